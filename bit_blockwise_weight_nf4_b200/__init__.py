@@ -6,10 +6,12 @@ quantize / dequantize / GEMV / GEMM path runs in the CUDA library:
 * raw ctypes entry points with the C names (``bnb_quantize_4bit``,
   ``bnb_quantize_4bit_noalloc``, ``bnb_dequantize_4bit``, ``bnb_gemv_4bit``,
   ``bnb_gemv_4bit_grouped``, ``bnb_gemm_4bit``,
-  ``bnb_linear_4bit``, ``bnb4_query_sizes``, ``bnb4_device_status``,
+  ``bnb_linear_4bit``, ``bnb_kv_write_4bit``, ``bnb_kv_read_4bit``,
+  ``bnb_attn_4bit``, ``bnb4_attn_workspace``, ``bnb4_query_sizes``, ``bnb4_device_status``,
   ``bnb4_strerror``, ``bnb4_abi_version``), returning the C status;
 * torch helpers (``QuantState``, ``quantize_4bit``, ``dequantize_4bit``,
-  ``gemv_4bit``, ``gemv_4bit_grouped``, ``gemm_4bit``, ``linear_4bit``) that
+  ``gemv_4bit``, ``gemv_4bit_grouped``, ``gemm_4bit``, ``linear_4bit``;
+  ``KVCache4bit``, ``kv_write_4bit``, ``kv_read_4bit``, ``attn_4bit``) that
   allocate device buffers
   with torch, call the entry points on torch's current stream and raise
   ``Bnb4Error`` on a non-zero status.
@@ -41,7 +43,7 @@ F32 = 0
 BF16 = 1
 F16 = 2
 
-ABI_VERSION = 4
+ABI_VERSION = 5
 GROUP_MAX = 256
 
 
@@ -65,6 +67,32 @@ class Sizes(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_size_t), ("absmax", ctypes.c_size_t),
                 ("absmax_q", ctypes.c_size_t), ("scale2", ctypes.c_size_t),
                 ("offset", ctypes.c_size_t), ("workspace", ctypes.c_size_t)]
+
+
+class KvCache(ctypes.Structure):
+    """``bnb4_kv_cache``: device pointers and sizes of a key/value cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_absmax", ctypes.c_void_p), ("v_absmax", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("blocksize", ctypes.c_int32), ("qtype", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Attn(ctypes.Structure):
+    """``bnb4_attn``: the arguments of an attention call."""
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride_t", ctypes.c_int64),
+                ("q_stride_h", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride_t", ctypes.c_int64), ("out_stride_h", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("cache", ctypes.POINTER(KvCache)),
+                ("block_table", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
+                ("seq_lens", ctypes.c_void_p), ("cu_seqlens_q", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("total_q", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("max_q_len", ctypes.c_int32),
+                ("max_seq_len", ctypes.c_int32), ("block_table_width", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
 class Bnb4Error(RuntimeError):
@@ -103,6 +131,12 @@ def load():
         "bnb4_debug_gemv_grouped_persistent": ([ctypes.POINTER(GemvProblem), i32, i64, i32, p],
                                                ctypes.c_int),
         "bnb_linear_4bit": ([p, i32, i64, i64, QP, i64, p, p, p], ctypes.c_int),
+        "bnb_kv_write_4bit": ([p, i64, i64, p, i64, i64, i64, p, ctypes.POINTER(KvCache), p],
+                              ctypes.c_int),
+        "bnb_kv_read_4bit": ([ctypes.POINTER(KvCache), p, i64, p, i64, i64, p, i64, i64, i32, p],
+                             ctypes.c_int),
+        "bnb4_attn_workspace": ([ctypes.POINTER(Attn), ctypes.POINTER(sz)], ctypes.c_int),
+        "bnb_attn_4bit": ([ctypes.POINTER(Attn), p], ctypes.c_int),
         "bnb4_device_status": ([p, i32], ctypes.c_int),
         "bnb4_debug_gemm_withhold": ([p, i64, i64, QP, i64, p, i32, p], ctypes.c_int),
         "bnb4_debug_check_rcp": ([p, p], ctypes.c_int),
@@ -185,6 +219,28 @@ def bnb4_debug_gemv_grouped_persistent(problems, B, dtype, stream):
 
 def bnb_linear_4bit(x, dtype, M, K, W, N, bias, y, stream):
     return load().bnb_linear_4bit(x, dtype, M, K, ctypes.byref(W), N, bias, y, stream)
+
+
+def bnb_kv_write_4bit(k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, tokens, slots,
+                      cache, stream):
+    return load().bnb_kv_write_4bit(k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, tokens,
+                                    slots, ctypes.byref(cache), stream)
+
+
+def bnb_kv_read_4bit(cache, slots, tokens, k, k_stride_t, k_stride_h, v, v_stride_t, v_stride_h,
+                     out_dtype, stream):
+    return load().bnb_kv_read_4bit(ctypes.byref(cache), slots, tokens, k, k_stride_t, k_stride_h,
+                                   v, v_stride_t, v_stride_h, out_dtype, stream)
+
+
+def bnb4_attn_workspace(args):
+    out = ctypes.c_size_t(0)
+    rc = load().bnb4_attn_workspace(ctypes.byref(args), ctypes.byref(out))
+    return rc, out.value
+
+
+def bnb_attn_4bit(args, stream):
+    return load().bnb_attn_4bit(ctypes.byref(args), stream)
 
 
 def bnb4_debug_gemm_withhold(X, M, K, W, N, Y, wait_limit_us, stream):
@@ -395,6 +451,211 @@ def gemv_4bit_grouped(items, outs=None, _persistent=False):
     rc = fn(probs, items[0][0].shape[0], dt, _stream())
     _check(rc, "bnb_gemv_4bit_grouped")
     return outs
+
+
+# --------------------------------------------------- key/value cache (torch)
+class _On:
+    """The device a call's tensors live on, made current while it runs."""
+
+    def __init__(self, device):
+        _need(device.type == "cuda", "the cache is not on a CUDA device")
+        self.cuda = _torch().cuda
+        self.device = device.index
+
+    def __enter__(self):
+        self.back = self.cuda.current_device()
+        if self.device != self.back:
+            self.cuda.set_device(self.device)
+        return self.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.device != self.back:
+            self.cuda.set_device(self.back)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+class KVCache4bit:
+    """A paged key/value cache in 4 bits: ``k_codes``, ``v_codes`` uint8
+    [pages, kv heads, page size, D / 2] and ``k_absmax``, ``v_absmax`` (the
+    cache's type, bf16 or fp16) [pages, kv heads, page size, D / blocksize],
+    contiguous CUDA tensors owned by the caller; the layout is that of
+    ``bnb4_kv_cache`` in include/bnb4.h.  ``KVCache4bit.empty`` allocates
+    one.  Slot s is row s % page_size of page s // page_size."""
+
+    def __init__(self, k_codes, v_codes, k_absmax, v_absmax, blocksize=64, qtype=NF4):
+        torch = _torch()
+        _need(k_codes.dim() == 4 and k_codes.dtype == torch.uint8,
+              "codes are uint8 [pages, kv heads, page size, D / 2]")
+        pages, heads, page, half = k_codes.shape
+        dt = {torch.bfloat16: BF16, torch.float16: F16}.get(k_absmax.dtype)
+        if dt is None:
+            raise TypeError("a cache's scales are bfloat16 or float16")
+        _need(v_codes.shape == k_codes.shape and v_codes.dtype == torch.uint8,
+              "k_codes and v_codes differ in shape or dtype")
+        _need(blocksize > 0 and k_absmax.shape == (pages, heads, page, 2 * half // blocksize),
+              "k_absmax is [pages, kv heads, page size, D / blocksize]")
+        _need(v_absmax.shape == k_absmax.shape and v_absmax.dtype == k_absmax.dtype,
+              "k_absmax and v_absmax differ in shape or dtype")
+        for t in (k_codes, v_codes, k_absmax, v_absmax):
+            _need(t.is_contiguous() and t.device == k_codes.device,
+                  "a cache's tensors are contiguous and on one device")
+        self.k_codes, self.v_codes = k_codes, v_codes
+        self.k_absmax, self.v_absmax = k_absmax, v_absmax
+        self.num_pages, self.n_kv_heads, self.page_size = pages, heads, page
+        self.head_dim, self.blocksize, self.qtype = 2 * half, blocksize, qtype
+        self.dtype, self.device = k_absmax.dtype, k_codes.device
+        self.struct = KvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_absmax.data_ptr(),
+                              v_absmax.data_ptr(), pages, page, heads, 2 * half, blocksize,
+                              qtype, dt, 0)
+
+    @staticmethod
+    def empty(num_pages, page_size, n_kv_heads, head_dim, dtype=None, blocksize=64, qtype=NF4,
+              device="cuda"):
+        torch = _torch()
+        dtype = dtype or torch.bfloat16
+        rows = (num_pages, n_kv_heads, page_size)
+        codes = [torch.empty(*rows, head_dim // 2, dtype=torch.uint8, device=device)
+                 for _ in range(2)]
+        scales = [torch.empty(*rows, head_dim // blocksize, dtype=dtype, device=device)
+                  for _ in range(2)]
+        return KVCache4bit(*codes, *scales, blocksize, qtype)
+
+    @property
+    def nbytes(self):
+        return sum(t.numel() * t.element_size()
+                   for t in (self.k_codes, self.v_codes, self.k_absmax, self.v_absmax))
+
+
+def _kv_rows(t, cache, tokens, what):
+    """(pointer, token stride, head stride) of k, v, q or out [T, H, D]."""
+    _need(t.dim() == 3 and t.shape[0] == tokens and t.shape[2] == cache.head_dim
+          and (t.stride(2) == 1 or t.numel() == 0),
+          "%s is [tokens, heads, %d] with a contiguous last dimension" % (what, cache.head_dim))
+    _need(t.device == cache.device, "%s is on another device than the cache" % what)
+    # the stride of a dimension of one is never used, and may be anything
+    return (t.data_ptr(), t.stride(0) if tokens > 1 else 0,
+            t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _index(t, cache, dtype, what):
+    _need(t.dtype == dtype and t.device == cache.device,
+          "%s is a %s tensor on the cache's device" % (what, dtype))
+    return t
+
+
+def kv_write_4bit(k, v, cache, slots):
+    """Quantize keys and values [T, kv heads, D] (the cache's dtype; any
+    token and head stride that is a multiple of 8) into the cache's slots
+    ``slots`` (int64 [T]; a slot outside the cache, such as -1, leaves its
+    token out; slots must differ)."""
+    torch = _torch()
+    T = k.shape[0]
+    _need(k.dtype == cache.dtype and v.dtype == cache.dtype, "k and v have the cache's dtype")
+    kr, vr = _kv_rows(k, cache, T, "k"), _kv_rows(v, cache, T, "v")
+    _need(k.shape[1] == cache.n_kv_heads and v.shape[1] == cache.n_kv_heads,
+          "k and v have the cache's heads")
+    _index(slots, cache, torch.int64, "slots")
+    _need(slots.shape == (T,) and slots.is_contiguous(), "slots is a contiguous [T]")
+    with _On(cache.device) as stream:
+        rc = bnb_kv_write_4bit(*kr, *vr, T, slots.data_ptr(), cache.struct, stream)
+    _check(rc, "bnb_kv_write_4bit")
+    return cache
+
+
+def kv_read_4bit(cache, slots, out_dtype=None, out=None):
+    """The cached keys and values of ``slots`` (int64 [T]) as two tensors [T,
+    kv heads, D] of ``out_dtype`` (fp32, bf16 or fp16; default the cache's
+    dtype), or into ``out`` = (k, v), either of which may be None.  Rows of a
+    slot outside the cache are not written."""
+    torch = _torch()
+    _index(slots, cache, torch.int64, "slots")
+    _need(slots.dim() == 1 and slots.is_contiguous(), "slots is a contiguous [T]")
+    T = slots.shape[0]
+    if out is None:
+        kv = torch.empty(2, T, cache.n_kv_heads, cache.head_dim, dtype=out_dtype or cache.dtype,
+                         device=cache.device)
+        out = kv[0], kv[1]
+    k, v = out
+    dt = None
+    rows = []
+    for t in (k, v):
+        if t is None:
+            rows += [None, 0, 0]
+            continue
+        d = _DT.get(str(t.dtype))
+        if d is None or (dt is not None and d != dt):
+            raise TypeError("kv_read_4bit writes float32, bfloat16 or float16")
+        dt = d
+        _need(t.shape[1] == cache.n_kv_heads, "out has the cache's heads")
+        rows += _kv_rows(t, cache, T, "out")
+    if dt is None:
+        raise ValueError("kv_read_4bit: neither k nor v asked for")
+    with _On(cache.device) as stream:
+        rc = bnb_kv_read_4bit(cache.struct, slots.data_ptr(), T, *rows, dt, stream)
+    _check(rc, "bnb_kv_read_4bit")
+    return k, v
+
+
+def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None,
+              max_seq_len=None, scale=None, causal=True, window=0, out=None, lse=None,
+              workspace=None):
+    """Attention of queries q [T, heads, D] (the cache's dtype) over the cache;
+    see bnb_attn_4bit in include/bnb4.h.  ``block_table`` int32 [B, W] (pages
+    of each sequence), ``seq_lens`` int32 [B] (its cached tokens, the queries'
+    own among them).  The queries are ragged by ``cu_seqlens_q`` (int32 [B +
+    1], with ``max_q_len``), or T / B for each sequence.  ``scale`` defaults
+    to 1 / sqrt(D); ``window`` > 0 limits how far back a query sees;
+    ``lse`` (fp32 [T, heads], contiguous) receives the log-sum-exp.
+    ``max_seq_len`` (default: what the block table holds) is the bound by
+    which the work is split."""
+    torch = _torch()
+    T = q.shape[0]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _need(q.dtype == cache.dtype and out.dtype == cache.dtype, "q and out have the cache's dtype")
+    qr, outr = _kv_rows(q, cache, T, "q"), _kv_rows(out, cache, T, "out")
+    heads = q.shape[1]
+    _need(out.shape[1] == heads, "out has another number of heads than q")
+    _index(block_table, cache, torch.int32, "block_table")
+    _index(seq_lens, cache, torch.int32, "seq_lens")
+    _need(block_table.dim() == 2 and block_table.stride(1) == 1 or block_table.shape[-1] == 1,
+          "block_table is [B, W] with contiguous rows")
+    B, W = block_table.shape
+    _need(seq_lens.shape == (B,) and seq_lens.is_contiguous(), "seq_lens is a contiguous [B]")
+    if cu_seqlens_q is None:
+        _need(B > 0 and T % B == 0 or T == 0, "without cu_seqlens_q every sequence has T / B queries")
+        max_q_len = T // B if T else 1
+        cu = None
+    else:
+        _index(cu_seqlens_q, cache, torch.int32, "cu_seqlens_q")
+        _need(cu_seqlens_q.shape == (B + 1,) and cu_seqlens_q.is_contiguous(),
+              "cu_seqlens_q is a contiguous [B + 1]")
+        cu = cu_seqlens_q.data_ptr()
+        if max_q_len is None:
+            max_q_len = max(1, T)
+    if lse is not None:
+        _index(lse, cache, torch.float32, "lse")
+        _need(lse.shape == (T, heads) and lse.is_contiguous(), "lse is a contiguous [T, heads]")
+    room = min(W * cache.page_size, 0x7fffffff)
+    a = Attn(*qr, *outr, None if lse is None else lse.data_ptr(),
+             ctypes.pointer(cache.struct), block_table.data_ptr(),
+             block_table.stride(0) if B > 1 else W, seq_lens.data_ptr(), cu, None, 0, T, B,
+             heads, max_q_len, room if max_seq_len is None else max_seq_len, W, int(bool(causal)),
+             window, cache.head_dim ** -0.5 if scale is None else scale, 0)
+    with _On(cache.device) as stream:
+        rc, size = bnb4_attn_workspace(a)
+        _check(rc, "bnb_attn_4bit")
+        if size:
+            if workspace is None:
+                workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        rc = bnb_attn_4bit(a, stream)
+    _check(rc, "bnb_attn_4bit")
+    return out
 
 
 def state_from_arrays(arrs, device="cuda"):

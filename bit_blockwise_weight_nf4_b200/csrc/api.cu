@@ -70,6 +70,7 @@ int error_word(int** out) {
 }  // namespace
 
 int bnb4::device_error_word(int** out) { return error_word(out); }
+int bnb4::device_sms(int* out) { return num_sms(out); }
 
 namespace {
 

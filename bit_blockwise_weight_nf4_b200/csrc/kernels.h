@@ -36,8 +36,10 @@ cudaError_t launch_quantize(const void* x, int x_dtype, const bnb4_qstate& st,
                             void* workspace, int* err, int num_sms, cudaStream_t s,
                             const View2D* view = nullptr, bool warm_x = false);
 
-// The library's device error word on the current device (api.cu).
+// The library's device error word on the current device, and the device's
+// number of SMs (api.cu).
 int device_error_word(int** out);
+int device_sms(int* out);
 
 int dequant_grid(int64_t n, int out_dtype, int num_sms);
 cudaError_t launch_dequantize(const bnb4_qstate& st, void* out, int out_dtype,

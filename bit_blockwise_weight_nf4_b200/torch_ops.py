@@ -7,6 +7,9 @@ the binding in ``__init__.py`` (no computation here, no CPU fallback).
   without double quantization.
 * ``torch.ops.bnb4.dequantize_4bit(codes, absmax, absmax_q, scale2, offset,
   n, blocksize, qtype, double_quant, out_dtype)`` -> flat tensor of n.
+* ``torch.ops.bnb4.kv_write_4bit`` (writes the cache's tensors in place),
+  ``kv_read_4bit`` -> (k, v) and ``attn_4bit`` -> out: the paged 4-bit
+  key/value cache, given by its four tensors, blocksize and qtype.
 * ``torch.ops.bnb4.gemv_4bit`` / ``gemm_4bit`` (bf16) and ``linear_4bit``
   (bf16 or fp16 with an optional bias): y = x @ What^T for a weight [N, K]
   given by its state tensors.
@@ -21,7 +24,8 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import (BF16, F16, NF4, QState, _check, _stream, bnb_dequantize_4bit, bnb_gemm_4bit,
+from . import (BF16, F16, KVCache4bit, NF4, QState, _check, attn_4bit as _attn_4bit,
+               kv_read_4bit as _kv_read_4bit, kv_write_4bit as _kv_write_4bit, _stream, bnb_dequantize_4bit, bnb_gemm_4bit,
                bnb_gemv_4bit, bnb_linear_4bit, bnb_quantize_4bit, bnb_quantize_4bit_2d,
                workspace_for, QuantState)
 
@@ -146,6 +150,55 @@ for _op in (gemv_4bit, gemm_4bit):
 @linear_4bit.register_fake
 def _(x, codes, absmax, absmax_q, scale2, offset, N, blocksize, qtype, double_quant, bias):
     return x.new_empty(x.shape[0], N)
+
+
+# ----------------------------------------------------------- key/value cache
+@torch.library.custom_op("bnb4::kv_write_4bit",
+                         mutates_args=("k_codes", "v_codes", "k_absmax", "v_absmax"))
+def kv_write_4bit(k: Tensor, v: Tensor, k_codes: Tensor, v_codes: Tensor, k_absmax: Tensor,
+                  v_absmax: Tensor, slots: Tensor, blocksize: int, qtype: int) -> None:
+    _kv_write_4bit(k, v, KVCache4bit(k_codes, v_codes, k_absmax, v_absmax, blocksize, qtype),
+                   slots)
+
+
+@kv_write_4bit.register_fake
+def _(k, v, k_codes, v_codes, k_absmax, v_absmax, slots, blocksize, qtype):
+    return None
+
+
+@torch.library.custom_op("bnb4::kv_read_4bit", mutates_args=())
+def kv_read_4bit(k_codes: Tensor, v_codes: Tensor, k_absmax: Tensor, v_absmax: Tensor,
+                 slots: Tensor, blocksize: int, qtype: int,
+                 out_dtype: torch.dtype) -> Tuple[Tensor, Tensor]:
+    cache = KVCache4bit(k_codes, v_codes, k_absmax, v_absmax, blocksize, qtype)
+    # slots outside the cache read as zeros here: an operator's output is whole
+    out = tuple(torch.zeros(slots.shape[0], cache.n_kv_heads, cache.head_dim, dtype=out_dtype,
+                            device=cache.device) for _ in range(2))
+    return _kv_read_4bit(cache, slots, out=out)
+
+
+@kv_read_4bit.register_fake
+def _(k_codes, v_codes, k_absmax, v_absmax, slots, blocksize, qtype, out_dtype):
+    shape = (slots.shape[0], k_codes.shape[1], 2 * k_codes.shape[3])
+    return tuple(k_codes.new_empty(shape, dtype=out_dtype) for _ in range(2))
+
+
+@torch.library.custom_op("bnb4::attn_4bit", mutates_args=())
+def attn_4bit(q: Tensor, k_codes: Tensor, v_codes: Tensor, k_absmax: Tensor, v_absmax: Tensor,
+              block_table: Tensor, seq_lens: Tensor, cu_seqlens_q: Optional[Tensor],
+              max_q_len: int, max_seq_len: int, scale: float, causal: bool, window: int,
+              blocksize: int, qtype: int) -> Tensor:
+    cache = KVCache4bit(k_codes, v_codes, k_absmax, v_absmax, blocksize, qtype)
+    # rows of no sequence are zeros here
+    out = None if cu_seqlens_q is None else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    return _attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q, max_q_len, max_seq_len,
+                      scale, causal, window, out=out)
+
+
+@attn_4bit.register_fake
+def _(q, k_codes, v_codes, k_absmax, v_absmax, block_table, seq_lens, cu_seqlens_q, max_q_len,
+      max_seq_len, scale, causal, window, blocksize, qtype):
+    return torch.empty(q.shape, dtype=q.dtype, device=q.device)
 
 
 # ------------------------------------------------------------------- module

@@ -62,7 +62,7 @@
 extern "C" {
 #endif
 
-#define BNB4_ABI_VERSION 4
+#define BNB4_ABI_VERSION 5
 
 /* Every entry point is exported from the shared library (the library is
  * built with hidden visibility by default). */
@@ -374,6 +374,134 @@ BNB4_API int bnb_gemm_4bit(const void* X, int64_t M, int64_t K, const bnb4_qstat
 BNB4_API int bnb_linear_4bit(const void* x, int32_t dtype, int64_t M, int64_t K,
                              const bnb4_qstate* W, int64_t N, const void* bias, void* y,
                              void* stream);
+
+/* --------------------------------------------- 4-bit key/value cache
+ *
+ * A paged cache of keys and values in 4 bits, written token by token or
+ * prompt by prompt, read back, and attended to.  The pages describe weights
+ * only; this is the same blockwise format for the attention between the
+ * 4-bit linears.
+ *
+ *  row       one key/value head's head_dim values of one token: blocks of
+ *            `blocksize` consecutive values, each quantized exactly as
+ *            bnb_quantize_4bit quantizes a block; the scale (absmax) is kept
+ *            in `dtype`, which holds it exactly.  A cached value is
+ *            RN(t[code] * absmax) in fp32.
+ *  k_codes, v_codes    uint8 [num_pages, n_kv_heads, page_size, head_dim/2]
+ *  k_absmax, v_absmax  dtype [num_pages, n_kv_heads, page_size,
+ *            head_dim/blocksize]; all four contiguous, 16-byte aligned,
+ *            device memory.
+ *  order     a row's codes lie two per byte, the first in the high nibble,
+ *            in 8 strips: strip s holds, block after block, values [s w,
+ *            (s + 1) w) of each block, w = blocksize / 8 (the natural order
+ *            when blocksize == head_dim).
+ *  slot      row s % page_size of page s / page_size.
+ */
+typedef struct bnb4_kv_cache {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  void* k_absmax;
+  void* v_absmax;
+  int64_t num_pages;  /* num_pages * page_size < 2^31 */
+  int32_t page_size;  /* a multiple of 16 */
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t blocksize;  /* 32, 64 or 128, at most head_dim */
+  int32_t qtype;      /* BNB4_NF4 or BNB4_FP4 */
+  int32_t dtype;      /* BNB4_BF16 or BNB4_F16: k, v, q, out, scales */
+  int32_t reserved;   /* must be 0 */
+} bnb4_kv_cache;
+
+/*
+ * Quantizes `tokens` tokens' keys and values into the cache: token t goes to
+ * slot slots[t]; a slot outside [0, num_pages * page_size) (padding, say -1)
+ * leaves the token out.  A slot given twice in one call ends with either
+ * token's values or a mixture of both.
+ *  k, v    cache->dtype, element (t, h, d) at t * stride_t + h * stride_h + d
+ *          (strides in elements, >= 0, multiples of 8; so a fused q/k/v
+ *          projection is read in place); 16-byte aligned device memory.
+ *  slots   int64[tokens], device.
+ * tokens = 0 returns BNB4_OK and launches nothing.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, SHAPE, CUDA.
+ */
+BNB4_API int bnb_kv_write_4bit(const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                               const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                               int64_t tokens, const int64_t* slots,
+                               const bnb4_kv_cache* cache, void* stream);
+
+/*
+ * The cached keys and values of `tokens` slots, dequantized to out_dtype
+ * (BNB4_F32, BNB4_BF16 or BNB4_F16): RN_out(RN(t[code] * absmax)).  k or v
+ * may be NULL (not read).  Rows of a slot outside the cache are left as they
+ * were.  Strides in elements, >= 0, multiples of 8 (4 for BNB4_F32).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, SHAPE, CUDA.
+ */
+BNB4_API int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, int64_t tokens,
+                              void* k, int64_t k_stride_t, int64_t k_stride_h, void* v,
+                              int64_t v_stride_t, int64_t v_stride_h, int32_t out_dtype,
+                              void* stream);
+
+/*
+ * Attention of new queries over the cache.  Sequence b has seq_lens[b] cached
+ * tokens, its queries' own among them as the last (write first, then attend);
+ * token j of it lies in page block_table[b * block_table_stride + j /
+ * page_size].  Query i of the n_b of a sequence stands at position p =
+ * seq_lens[b] - n_b + i and sees the tokens j < seq_lens[b] with, if causal,
+ * j <= p and, if window > 0, j > p - window:
+ *   out = sum_j softmax_j(scale * q . K_j) V_j
+ * with K and V the cached values, unrounded, sums in fp32 and one rounding to
+ * dtype.  Head h of n_heads attends to key/value head h / (n_heads /
+ * n_kv_heads).  A query that sees nothing (an empty sequence, one shorter
+ * than its queries) gives zeros and a log-sum-exp of -infinity.
+ *  cu_seqlens_q  int32[batch + 1]: sequence b's queries are rows
+ *          [cu_seqlens_q[b], cu_seqlens_q[b + 1]) of q and out; or NULL:
+ *          max_q_len each (total_q = batch * max_q_len).  Rows of no sequence
+ *          are left as they were, and so are a sequence's rows behind its
+ *          first max_q_len.
+ *  seq_lens      int32[batch]; lengths past block_table_width * page_size
+ *          are cut there, negative ones are 0.
+ *  block_table   tokens of a page entry outside [0, num_pages) are not seen.
+ *  max_seq_len   the caller's bound of seq_lens, by which the work is split;
+ *          any value gives right results.
+ *  lse     float[total_q, n_heads], natural logarithm of the row's sum of
+ *          exp(scale * q . K_j), or NULL.
+ *  workspace     bnb4_attn_workspace bytes (0: may be NULL), 16-byte aligned,
+ *          any contents; not to be shared by calls that may overlap.
+ * All device memory; q and out 16-byte aligned, strides in elements, >= 0,
+ * multiples of 8.  Finite scales are taken up to 2^100.  Results repeat bit
+ * for bit on a device.  The call reads seq_lens, cu_seqlens_q and block_table
+ * on the device, so a captured graph may be replayed with other lengths.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, SHAPE, WORKSPACE, CUDA.
+ */
+typedef struct bnb4_attn {
+  const void* q;
+  int64_t q_stride_t, q_stride_h;
+  void* out;
+  int64_t out_stride_t, out_stride_h;
+  float* lse;
+  const bnb4_kv_cache* cache;
+  const int32_t* block_table;
+  int64_t block_table_stride; /* >= block_table_width */
+  const int32_t* seq_lens;
+  const int32_t* cu_seqlens_q;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t total_q;
+  int32_t batch;
+  int32_t n_heads;
+  int32_t max_q_len;
+  int32_t max_seq_len;
+  int32_t block_table_width;
+  int32_t causal;  /* 0 or 1 */
+  int32_t window;  /* 0: none */
+  float scale;     /* > 0 */
+  int32_t reserved; /* must be 0 */
+} bnb4_attn;
+
+/* Fills *bytes with the workspace of the call (its pointers are not looked
+ * at, the cache's sizes and the row counts are).  Pure host function. */
+BNB4_API int bnb4_attn_workspace(const bnb4_attn* a, size_t* bytes);
+BNB4_API int bnb_attn_4bit(const bnb4_attn* a, void* stream);
 
 /*
  * Synchronizes `stream`, then reads the library's device error word of the
