@@ -126,7 +126,7 @@ static int check_attn(const bnb4_attn* a) {
     return BNB4_ERR_SHAPE;
   if (a->block_table_width < 1 || a->block_table_stride < a->block_table_width)
     return BNB4_ERR_SHAPE;
-  if (!(a->scale > 0.0f && a->scale < 1e30f)) return BNB4_ERR_INVALID_ARG;
+  if (!(a->scale >= 1e-8f && a->scale <= 1e8f)) return BNB4_ERR_INVALID_ARG;
   return BNB4_OK;
 }
 

@@ -7,10 +7,15 @@
 // over the tokens j a row sees; t is the 16-entry code table.
 //
 // Design.
-//  * The cache is read once: every warp walks tiles of kTile tokens of one
-//    (sequence, key/value head), codes straight from global memory into
-//    registers one tile ahead, with its own running maximum and sums; the
-//    CTA's warps join in shared memory at the end of a segment.
+//  * The cache is read once.  A CTA's warps form two groups; a group walks the
+//    tiles of kTile tokens of one (sequence, key/value head), warp by warp,
+//    each with its own running maximum and sums, and joins in shared memory
+//    at the end of a segment while the other group's loads keep going.
+//  * A warp brings its tiles into its own part of shared memory with bulk
+//    copies (one for the codes and one for the scales of 16 tokens, issued
+//    by one lane each), keys while the values before them are multiplied and
+//    values while the scores form, so neither registers nor address
+//    arithmetic of the other lanes are spent on them.
 //  * Products run on mma.sync m16n8k16 (fp16 in, fp32 sums) with the cache as
 //    the A operand -- 16 tokens of K, or 16 dimensions of V -- and up to 8
 //    rows of q or p as B, so that no multiply is spent on padding to 16 rows.
@@ -39,6 +44,7 @@
 #include "common.cuh"
 #include "kvcache.h"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace bnb4 {
 namespace {
@@ -123,6 +129,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -141,195 +154,278 @@ __device__ __forceinline__ float lg2(float x) {
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
-// The fp16 pair of a code byte: {t[byte >> 4], t[byte & 15]} from the table
-// at shared address 64 KB, entry `byte` in 256 bytes, one copy per bank.
-// lane_base: bytes {4 * lane, 0, 1, 0}; the permute puts byte I of w between.
+constexpr uint32_t kTilesAt = 0x1000;   // shared address behind the static arrays
+constexpr uint32_t kTableAt = 0x10000;  // and of the pair table
+
+// Address in the table of a code byte's fp16 pair {t[byte >> 4], t[byte &
+// 15]}: entry `byte` has 256 bytes, of which the first 128 hold a copy for
+// each bank.  lane_base: bytes {4 * lane, 0, 1, 0}; the permute puts byte I of
+// w between.
 template <int I>
-__device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_base) {
-  uint32_t at, v;
+__device__ __forceinline__ uint32_t entry_of(uint32_t w, uint32_t lane_base) {
+  uint32_t at;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(at) : "r"(w), "r"(lane_base), "n"(0x7604 | (I << 4)));
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return at;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t pair_at(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(v) : "r"(at), "n"(OFF));
   return v;
 }
-
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+template <int I>
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_base) {
+  return pair_at<0>(entry_of<I>(w, lane_base));
 }
 
-constexpr uint32_t kTableAt = 0x10000;   // shared address of the pair table
-constexpr uint32_t kJoinAt = 0x20000;    // and of the warps' partial outputs
-// The code table times this constant rounds to fp16 with a root mean square
-// error of 6.2e-5 of the values' (1.6e-4 as it stands); FP4's magnitudes
-// times 6 are E2M1's, exact.
-constexpr float kNf4Scale = 1.67768975f;
+// The code table times this constant rounds to fp16 within 3.1e-4 of a value,
+// exactly at the block's largest (1 and -1), with a root mean square error of
+// 3.6e-5 of the scale (as it stands: 7e-5); of the constants with exact ends
+// it leaves the least error in attention over normal keys (simulated: 2.0e-4
+// of the output against 4.3e-4).  FP4's magnitudes times 6 are E2M1's, exact.
+constexpr float kNf4Scale = 1613.0f / 1024.0f;
 constexpr float kFp4Scale = 6.0f;
 
+// KR: the second 128 bytes of an entry hold what the first rounded away.
+template <bool KR>
 __device__ __forceinline__ void build_table(int qtype, int warps) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane & 15;
   const float v = qtype == kQtNF4 ? __fmul_rn(nf4_value(c), kNf4Scale)
                                   : rintf(__fmul_rn(code_value(kQtFP4, c), 12.0f)) * 0.5f;
   const uint32_t h = pack_f16x2(v, 0.0f) & 0xffffu;
+  // exact: v is within half an fp16 step of h
+  const uint32_t r = pack_f16x2(__fsub_rn(v, half_to_f32<BNB4_F16>(h)), 0.0f) & 0xffffu;
   for (int e = warp; e < 256; e += warps) {
-    const uint32_t hi = __shfl_sync(0xffffffffu, h, e >> 4);
-    const uint32_t lo = __shfl_sync(0xffffffffu, h, e & 15);
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(kTableAt + 256u * e + 4u * lane),
-                 "r"(hi | lo << 16)
-                 : "memory");
+    const uint32_t at = kTableAt + 256u * e + 4u * lane;
+    const uint32_t x = __shfl_sync(0xffffffffu, h, e >> 4) | __shfl_sync(0xffffffffu, h, e & 15) << 16;
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
+    if constexpr (KR) {
+      const uint32_t y =
+          __shfl_sync(0xffffffffu, r, e >> 4) | __shfl_sync(0xffffffffu, r, e & 15) << 16;
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128u), "r"(y) : "memory");
+    }
   }
 }
 
 template <int BYTES>
 struct Chunk {  // 4, 8 or 16 bytes of codes
   uint32_t w[BYTES / 4];
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (BYTES == 16) {
-      const uint4 v = ldg_stream_v4(p);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (BYTES == 8) {
-      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                   : "=r"(w[0]), "=r"(w[1])
-                   : "l"(p));
+  __device__ __forceinline__ void load(uint32_t at) {  // shared address
+    if constexpr (BYTES == 16)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(at));
+    else if constexpr (BYTES == 8)
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    else
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+  }
+};
+
+// The NB scales of one token: raw 16-bit patterns, two per word.
+template <int NB>
+struct Scales {
+  uint32_t w[(NB + 1) / 2];
+  __device__ __forceinline__ void load(uint32_t at) {
+    if constexpr (NB == 1) {
+      uint16_t x;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at));
+      w[0] = x;
+    } else if constexpr (NB == 2) {
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
     } else {
-      asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
     }
   }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < BYTES / 4; ++i) w[i] = 0u;
+  template <int F>
+  __device__ __forceinline__ float at(int b) const {
+    const uint32_t x = w[b / 2];
+    if constexpr (F == BNB4_BF16)
+      return (b & 1) ? bf16_hi(x) : bf16_lo(x);
+    else
+      return half_to_f32<F>((b & 1) ? x >> 16 : x & 0xffffu);
   }
 };
 
-// NB scales of one cache row (2, 4 or 8 bytes)
-template <int NB>
-__device__ __forceinline__ void load_scales(const uint16_t* p, uint32_t (&s)[(NB + 1) / 2]) {
-  if constexpr (NB == 1) {
-    s[0] = __ldg(p);
-  } else if constexpr (NB == 2) {
-    s[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  } else {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    s[0] = v.x;
-    s[1] = v.y;
-  }
+__device__ __forceinline__ void copy_to_shared(uint32_t dst, const void* src, uint32_t bytes,
+                                               uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
-template <int F, int NB>
-__device__ __forceinline__ float scale_at(const uint32_t (&s)[(NB + 1) / 2], int b) {
-  const uint32_t w = s[b / 2];
-  return half_to_f32<F>((b & 1) ? w >> 16 : w & 0xffffu);
+__device__ __forceinline__ void group_sync(int group, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
 }
 
-// One warp tile's codes and scales in flight.
-template <int D, int NB, int NS>
-struct TileRegs {
-  Chunk<D / 8> k[NS][2];
-  Chunk<D / 16> v[NS][4];
-  uint32_t ka[NS][2][(NB + 1) / 2], va[NS][2][(NB + 1) / 2];
-};
-
-// Values d .. d + 3 of row r of (sequence, key/value head): v over its sum of
-// weights (relative to 2^top).  A row that saw no token has top = -infinity
-// and sum 0 (a NaN score leaves a NaN sum) and gives zeros.
+// Where row r of (sequence, key/value head) goes, divided by its sum of weights
+// (relative to 2^top).  A row that saw no token has top = -infinity and sum 0
+// (a NaN score leaves a NaN sum) and gives zeros.
 template <int F>
-__device__ __forceinline__ void store_row(const DecodeArgs& a, const Span& sp, int h, int r, int d,
-                                          const float4& v, float top, float sum) {
-  const int i = r / a.group, hh = r - i * a.group;
-  const bool sees = top != -INFINITY || sum != 0.0f;
-  const float inv = 1.0f / sum;
-  const int64_t tok = static_cast<int64_t>(sp.q0) + i;
-  const int head = h * a.group + hh;
-  uint2 w;
-  w.x = sees ? pack2<F>(v.x * inv, v.y * inv) : 0u;
-  w.y = sees ? pack2<F>(v.z * inv, v.w * inv) : 0u;
-  *reinterpret_cast<uint2*>(a.out + tok * a.o_ts + head * a.o_hs + d) = w;
-  if (a.lse && d == 0)
-    a.lse[tok * (static_cast<int64_t>(a.heads) * a.group) + head] =
-        sees ? (top + lg2(sum)) * 0.693147180559945f : -INFINITY;
-}
+struct RowOut {
+  uint16_t* at;
+  float inv;
+  bool sees;
+  __device__ __forceinline__ RowOut(const DecodeArgs& a, const Span& sp, int h, int r, float top,
+                                    float sum, bool write_lse) {
+    const int i = r / a.group, hh = r - i * a.group;
+    const int64_t tok = static_cast<int64_t>(sp.q0) + i;
+    const int head = h * a.group + hh;
+    sees = top != -INFINITY || sum != 0.0f;
+    inv = 1.0f / sum;
+    at = a.out + tok * a.o_ts + head * a.o_hs;
+    if (write_lse && a.lse)
+      a.lse[tok * (static_cast<int64_t>(a.heads) * a.group) + head] =
+          sees ? (top + lg2(sum)) * 0.693147180559945f : -INFINITY;
+  }
+  __device__ __forceinline__ void pair(int d, float x, float y) const {
+    *reinterpret_cast<uint32_t*>(at + d) = sees ? pack2<F>(x * inv, y * inv) : 0u;
+  }
+};
 
 // ------------------------------------------------------------- the kernel
 // D, BS: head dimension and block size.  F: the 16-bit type.  NT: 8-row
-// groups of the row tile.  NS: 16-token sub-tiles per tile.  W: warps.
-template <int D, int BS, int F, int NT, int NS, int W>
-__global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs a) {
-  constexpr int RT = 8 * NT, TILE = 16 * NS, NB = D / BS;
-  constexpr int KS = D / 16;  // k-steps of q.K; m-tiles of the output
+// groups of the row tile.  KR: the keys' table entries keep their rounding
+// residue in a second fp16 (fp16 caches with the NF4 table).
+template <int D, int BS, int F, int NT, bool KR>
+struct Shape {
+  static constexpr int NS = NT == 1 ? 4 : 2;           // 16-token sub-tiles per tile
+  static constexpr int ST = NT == 1 ? 1 : 2;           // tiles in flight per warp
+  static constexpr int W = NT == 1 && !KR ? 16 : 12;   // warps
+  static constexpr int GW = W / 2;                     // warps per group
+  static constexpr int RT = 8 * NT, TILE = 16 * NS, NB = D / BS, KS = D / 16;
+  static constexpr int kCodes = TILE * D / 2, kScales = TILE * NB * 2;
+  static constexpr int kStage = kCodes + kScales;      // one tile of keys, or of values
+  static constexpr int kWarp = 2 * ST * kStage;
+  // joining: up to kGive of a group's warps hand over at a time, one 128-byte
+  // piece per accumulator register
+  static constexpr int kGive = NT == 1 ? GW / 2 : 2;
+  static constexpr int kPieces = kGive * KS * NT * 4;
+  // where the table's entries use only half of their 256 bytes the pieces lie
+  // in the other half, else behind the warps' tiles
+  static constexpr bool kGaps = !KR && 2 * kPieces <= 256;
+  // shared addresses: the first warps' tiles below the table, the others' above
+  static constexpr int kBelow =
+      static_cast<int>(kTableAt - kTilesAt) / kWarp < W ? static_cast<int>(kTableAt - kTilesAt) / kWarp : W;
+  static constexpr uint32_t kAbove = kTableAt + 0x10000;
+  static constexpr uint32_t kJoin = kAbove + (W - kBelow) * kWarp;
+  static constexpr uint32_t kEnd = kJoin + (kGaps ? 0 : 2 * kPieces * 128);
+  __device__ static __forceinline__ uint32_t tiles(int warp) {
+    return warp < kBelow ? kTilesAt + static_cast<uint32_t>(warp) * kWarp
+                         : kAbove + static_cast<uint32_t>(warp - kBelow) * kWarp;
+  }
+  __device__ static __forceinline__ uint32_t piece(int group, int i) {
+    const uint32_t p = static_cast<uint32_t>(group * kPieces + i);
+    return kGaps ? kTableAt + 128u + 256u * p : kJoin + 128u * p;
+  }
+};
+
+struct Ctl {  // the fields that a bounded wait looks at
+  uint64_t wait_limit_ns;
+  int abort;
+};
+
+template <int D, int BS, int F, int NT, bool KR>
+__global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
+    attn_decode_kernel(const DecodeArgs a) {
+  using S = Shape<D, BS, F, NT, KR>;
+  constexpr int NS = S::NS, ST = S::ST, W = S::W, GW = S::GW, RT = S::RT, TILE = S::TILE;
+  constexpr int NB = S::NB, KS = S::KS;
   constexpr int SW = BS / 8;  // values of a block per strip
   constexpr bool kSplitP = F == BNB4_F16;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float sm_m[W][RT], sm_l[W][RT], sm_max[RT], sm_sum[RT];
-  __shared__ int sm_item[4];
+  __shared__ uint64_t bars[W][2 * ST];
+  __shared__ Ctl ctl;
+  __shared__ float sm_m[W][RT], sm_l[W][RT], sm_max[2][RT], sm_sum[2][RT];
+  __shared__ int sm_item[2][4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int grp = warp / GW, gw = warp - grp * GW;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t lane_base = kTableAt | (4u * lane);
-  // the table's fixed place must lie behind the static arrays and inside the
-  // dynamic ones (the launch asks for enough); refused here if it does not
-  if (smem_addr(smem_raw) > kTableAt || smem_addr(sm_m) >= kTableAt ||
-      smem_addr(sm_item) >= kTableAt) {
+  // the fixed places must lie behind the static arrays and inside the dynamic
+  // ones (the launch asks for enough); refused here if they do not
+  if (smem_u32(smem_raw) > kTilesAt || smem_u32(bars) + sizeof(bars) > kTilesAt ||
+      smem_u32(&ctl) + sizeof(ctl) > kTilesAt || smem_u32(sm_m) + sizeof(sm_m) > kTilesAt ||
+      smem_u32(sm_l) + sizeof(sm_l) > kTilesAt || smem_u32(sm_max) + sizeof(sm_max) > kTilesAt ||
+      smem_u32(sm_sum) + sizeof(sm_sum) > kTilesAt || smem_u32(sm_item) + sizeof(sm_item) > kTilesAt) {
     if (threadIdx.x == 0) atomicExch(a.err, 1);
     return;
   }
   pdl_trigger();
-  build_table(a.qtype, W);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 2 * ST; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    ctl.wait_limit_ns = kWaitLimitNs;
+    ctl.abort = 0;
+  }
+  build_table<KR>(a.qtype, W);
   pdl_wait();
 
-  // -------- this CTA's run of the line of tiles, or its items in turn
-  int64_t left;                  // tiles left of the run (split)
-  int b = 0, h = 0, rt = 0, tile0 = 0;
-  int64_t item = blockIdx.x;     // without split: (rt, h, b) in turn
-  const int64_t items = static_cast<int64_t>(a.batch) * a.heads * a.row_tiles;
-  if (a.split) {
-    if (warp == 0) {
-      int64_t total = 0;
+  // -------- this group's run of the line of tiles, or its items in turn
+  const int run = static_cast<int>(blockIdx.x) * 2 + grp, runs = 2 * static_cast<int>(gridDim.x);
+  if (a.split && gw == 0) {
+    int64_t total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int i = b0 + lane;
+      total += i < a.batch ? static_cast<int64_t>(span_of<RT, TILE>(a, i, 0).tiles) : 0;
+    }
+    total = warp_sum(total) * a.heads;
+    const int64_t per = (total + runs - 1) / runs;
+    const int64_t u0 = per * run;
+    const int64_t mine = u0 >= total ? 0 : total - u0 < per ? total - u0 : per;
+    int64_t before = 0;
+    int fb = 0, fh = 0, ft = 0;
+    if (mine > 0) {
       for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int i = b0 + lane;
-        total += i < a.batch ? static_cast<int64_t>(span_of<RT, TILE>(a, i, 0).tiles) : 0;
-      }
-      total = warp_sum(total) * a.heads;
-      const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-      const int64_t u0 = per * blockIdx.x;
-      const int64_t mine = u0 >= total ? 0 : total - u0 < per ? total - u0 : per;
-      int64_t before = 0;
-      int fb = 0, fh = 0, ft = 0;
-      if (mine > 0) {
-        for (int b0 = 0; b0 < a.batch; b0 += 32) {
-          const int i = b0 + lane;
-          const int tl = i < a.batch ? span_of<RT, TILE>(a, i, 0).tiles : 0;
-          int64_t incl = static_cast<int64_t>(tl) * a.heads;
+        const int tl = i < a.batch ? span_of<RT, TILE>(a, i, 0).tiles : 0;
+        int64_t incl = static_cast<int64_t>(tl) * a.heads;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          const unsigned past = __ballot_sync(0xffffffffu, before + incl > u0);
-          if (past) {
-            const int f = __ffs(past) - 1;
-            const int tf = __shfl_sync(0xffffffffu, tl, f);
-            const int64_t start =
-                before + __shfl_sync(0xffffffffu, incl, f) - static_cast<int64_t>(tf) * a.heads;
-            const int64_t x = u0 - start;
-            fb = b0 + f;
-            fh = static_cast<int>(x / tf);
-            ft = static_cast<int>(x - static_cast<int64_t>(fh) * tf);
-            break;
-          }
-          before += __shfl_sync(0xffffffffu, incl, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
         }
-      }
-      if (lane == 0) {
-        sm_item[0] = fb;
-        sm_item[1] = fh;
-        sm_item[2] = ft;
-        sm_item[3] = static_cast<int>(mine);
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > u0);
+        if (past) {
+          const int f = __ffs(past) - 1;
+          const int tf = __shfl_sync(0xffffffffu, tl, f);
+          const int64_t start =
+              before + __shfl_sync(0xffffffffu, incl, f) - static_cast<int64_t>(tf) * a.heads;
+          const int64_t x = u0 - start;
+          fb = b0 + f;
+          fh = static_cast<int>(x / tf);
+          ft = static_cast<int>(x - static_cast<int64_t>(fh) * tf);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    __syncthreads();
-    b = sm_item[0], h = sm_item[1], tile0 = sm_item[2];
-    left = sm_item[3];
-  } else {
-    left = 1;
-    __syncthreads();
+    if (lane == 0) {
+      sm_item[grp][0] = fb;
+      sm_item[grp][1] = fh;
+      sm_item[grp][2] = ft;
+      sm_item[grp][3] = static_cast<int>(mine);
+    }
   }
+  __syncthreads();
+  int b = 0, h = 0, rt = 0, tile0 = 0, left = 1;
+  int64_t item = run;
+  const int64_t items = static_cast<int64_t>(a.batch) * a.heads * a.row_tiles;
+  if (a.split) {
+    b = sm_item[grp][0], h = sm_item[grp][1], tile0 = sm_item[grp][2];
+    left = sm_item[grp][3];
+  }
+
+  // this warp's tiles: ST of keys, then ST of values
+  const uint32_t my_k = S::tiles(warp);
+  const uint32_t my_v = my_k + ST * S::kStage;
+  uint32_t put = 0, got = 0;  // tiles issued and consumed; slot = count % ST
+  bool ok_all = true;         // no wait gave up
 
   for (;;) {
     if (a.split) {
@@ -340,19 +436,74 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
       const int64_t x = item / a.row_tiles;
       h = static_cast<int>(x % a.heads);
       b = static_cast<int>(x / a.heads);
-      item += gridDim.x;
+      item += runs;
     }
     const Span sp = span_of<RT, TILE>(a, b, rt);
-    if (sp.rows == 0) {  // uniform over the CTA
+    if (sp.rows == 0) {  // uniform over the group
       if (a.split) ++b, h = 0, tile0 = 0;  // holds no tiles
       continue;
     }
-    const int tile1 = !a.split || sp.tiles - tile0 <= left ? sp.tiles
-                                                           : tile0 + static_cast<int>(left);
+    const int tile1 = !a.split || sp.tiles - tile0 <= left ? sp.tiles : tile0 + left;
+    const int32_t* bt = a.block_table + static_cast<int64_t>(b) * a.bt_stride;
+
+    // page of sub-tile `lane` of tile i; -1: no token of it is cached
+    auto page_of = [&](int i) {
+      int pg = -1;
+      if (lane < NS && i < tile1) {
+        const int j = sp.base + i * TILE + 16 * lane;
+        if (j < sp.end) {
+          const int p = __ldg(bt + a.page.div(static_cast<uint32_t>(j)));
+          if (p >= 0 && p < a.num_pages) pg = p;
+        }
+      }
+      return pg;
+    };
+    // copies of tile i's keys (or values) into the slot `n % ST`: lanes 2 s
+    // and 2 s + 1 bring sub-tile s's codes and scales
+    auto issue = [&](int i, int pages, uint32_t n, bool values) {
+      const uint32_t at = (values ? my_v : my_k) + (n % ST) * S::kStage;
+      const uint32_t bar = smem_u32(&bars[warp][(values ? ST : 0) + n % ST]);
+      const unsigned have = __ballot_sync(0xffffffffu, pages >= 0);
+      if (lane == 0)
+        mbar_arrive_expect_tx(bar, __popc(have) * (S::kCodes / NS + S::kScales / NS));
+      const int s = lane >> 1;
+      const int pg = __shfl_sync(0xffffffffu, pages, s);  // orders the reads before, too
+      if (s < NS && pg >= 0) {
+        const uint32_t j = static_cast<uint32_t>(sp.base + i * TILE + 16 * s);
+        const uint32_t in = j - a.page.div(j) * a.page.d;
+        const int64_t row = (static_cast<int64_t>(pg) * a.heads + h) * a.page.d + in;
+        if (lane & 1)
+          copy_to_shared(at + S::kCodes + s * (S::kScales / NS),
+                         (values ? a.v_absmax : a.k_absmax) + row * NB, S::kScales / NS, bar);
+        else
+          copy_to_shared(at + s * (S::kCodes / NS), (values ? a.v_codes : a.k_codes) + row * (D / 2),
+                         S::kCodes / NS, bar);
+      }
+      return have;
+    };
+    auto wait = [&](uint32_t n, bool values) {
+      const uint32_t bar = smem_u32(&bars[warp][(values ? ST : 0) + n % ST]);
+      if (!wait_bounded(bar, (n / ST) & 1, &ctl, a.err)) ok_all = false;
+      __syncwarp();
+    };
+
+    // the first tiles are on their way while q is read
+    unsigned have = 0;  // sub-tiles present, NS bits per tile in flight, oldest lowest
+#pragma unroll
+    for (int x = 0; x < ST; ++x) {
+      const int i = tile0 + gw + x * GW;
+      if (i < tile1 && ok_all) {  // after a failed wait nothing more is issued, but
+        const int pages = page_of(i);  // the group's barriers below are still met
+        have |= issue(i, pages, put, false) << (NS * x);
+        issue(i, pages, put, true);
+        ++put;
+      }
+    }
+    int pages_next = page_of(tile0 + gw + ST * GW);
 
     // ---------------- q: rows g (and g + 8) as the B operand of every k-step
     uint32_t qf[NT][KS][2];
-    float qs[NT][2];  // per column 2 t, 2 t + 1: s = (sum of products) * qs, in log2 units
+    float qs[NT][2];  // per column 2 t, 2 t + 1: score in log2 units = sum of products * qs
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = sp.r0 + 8 * n + g;
@@ -371,17 +522,20 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
           const int strip = p / (D / 8), x = p % (D / 8);
           const int d = (x / SW) * BS + strip * SW + x % SW;
           raw[s][e] = real ? __ldg(reinterpret_cast<const uint32_t*>(src + d)) : 0u;
-          const uint32_t m0 = raw[s][e] & 0x7fffu, m1 = (raw[s][e] >> 16) & 0x7fffu;
-          top = max(top, max(m0, m1));
         }
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          top = max(top, max(raw[s][e] & 0x7fffu, (raw[s][e] >> 16) & 0x7fffu));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       float mul = a.scale_log2;
       if constexpr (F == BNB4_BF16) {
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = static_cast<int>(top >> 7) - 127;  // exponent of the row's largest
         e = e < -100 ? -100 : e;
-        const float f = pow2(14 - e > 126 ? 126 : 14 - e);
-        mul *= pow2(e - 14 < -126 ? -126 : e - 14);
+        const float f = pow2(14 - e);
+        mul *= pow2(e - 14);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -390,8 +544,6 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
       } else {
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[n][s][0] = raw[s][0], qf[n][s][1] = raw[s][1];
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       }
       // a row with an infinite or NaN entry is NaN, whatever its products are
       if (top >= (F == BNB4_BF16 ? 0x7f80u : 0x7c00u)) mul = __int_as_float(0x7fffffff);
@@ -400,23 +552,10 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
       qs[n][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
       qs[n][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
     }
-    // last token (inclusive) and first each column sees
-    int see_hi[NT][2], see_lo[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 8 * n + 2 * t + c;
-        const int pos = sp.first + (sp.r0 + r) / a.group;
-        see_hi[n][c] = r >= sp.rows ? -1 : a.causal && pos < sp.len ? pos : sp.len - 1;
-        see_lo[n][c] = a.window > 0 ? pos - a.window + 1 : 0;
-      }
     // tokens every row sees: tiles inside need no mask
     const int pos0 = sp.first + sp.r0 / a.group;
     const int all_hi = a.causal && pos0 < sp.len ? pos0 : sp.len - 1;
     const int all_lo = a.window > 0 ? sp.first + (sp.r0 + sp.rows - 1) / a.group - a.window + 1 : 0;
-
-    const int32_t* bt = a.block_table + static_cast<int64_t>(b) * a.bt_stride;
 
     float m[NT][2], l[NT][2];
     float o[KS][NT][4];
@@ -434,184 +573,132 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
 #pragma unroll
     for (int i = 0; i < NB; ++i) ve[i] = -100;
 
-    // lane's rows of a sub-tile: MMA row g is token tok_g, row g + 8 is 8 + tok_g
-    const int tok_g = (g & 1) * 4 + (g >> 1);
+    // MMA row r of a sub-tile is its token r ^ (r >> 1 & 1): neighbouring rows
+    // differ in parity (keys), and so do rows 2 t and 2 t + 2 (values), which
+    // spreads their 64-byte rows over the banks
+    const int tok_g = g ^ ((g >> 1) & 1);
 
-    // page of each sub-tile of tile i (lane s < NS holds sub-tile s's), -1: none
-    auto pages_of = [&](int i) {
-      int pg = -1;
-      if (lane < NS && i < tile1) {
-        const int j = sp.base + i * TILE + 16 * lane;
-        if (j < sp.end) {
-          const uint32_t x = a.page.div(static_cast<uint32_t>(j));
-          const int p = __ldg(bt + x);
-          if (p >= 0 && p < a.num_pages) pg = p;
-        }
-      }
-      return pg;
-    };
-    TileRegs<D, NB, NS> cur;
-    uint32_t ok_k = 0, ok_v = 0;
-    auto row_at = [&](int i, int s, int pg) {
-      const uint32_t j = static_cast<uint32_t>(sp.base + i * TILE + 16 * s);
-      const uint32_t in = j - a.page.div(j) * a.page.d;
-      return (static_cast<int64_t>(pg) * a.heads + h) * a.page.d + in;
-    };
-    auto load_k = [&](int i, int pages) {
-      ok_k = 0;
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int pg = __shfl_sync(0xffffffffu, pages, s);
-        if (pg >= 0) {
-          ok_k |= 1u << s;
-          const int64_t row = row_at(i, s, pg) + tok_g;
-          cur.k[s][0].load(a.k_codes + row * (D / 2) + t * (D / 8));
-          cur.k[s][1].load(a.k_codes + (row + 8) * (D / 2) + t * (D / 8));
-          load_scales<NB>(a.k_absmax + row * NB, cur.ka[s][0]);
-          load_scales<NB>(a.k_absmax + (row + 8) * NB, cur.ka[s][1]);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            cur.k[s][x].zero();
-#pragma unroll
-            for (int y = 0; y < (NB + 1) / 2; ++y) cur.ka[s][x][y] = 0u;
-          }
-        }
-      }
-    };
-    auto load_v = [&](int i, int pages) {
-      ok_v = 0;
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int pg = __shfl_sync(0xffffffffu, pages, s);
-        if (pg >= 0) {
-          ok_v |= 1u << s;
-          const int64_t row = row_at(i, s, pg);
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            cur.v[s][c].load(a.v_codes + (row + 4 * c + t) * (D / 2) + g * (D / 16));
-          load_scales<NB>(a.v_absmax + (row + tok_g) * NB, cur.va[s][0]);
-          load_scales<NB>(a.v_absmax + (row + tok_g + 8) * NB, cur.va[s][1]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) cur.v[s][c].zero();
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int y = 0; y < (NB + 1) / 2; ++y) cur.va[s][x][y] = 0u;
-        }
-      }
-    };
-
-    int i = tile0 + warp;
-    int pages = pages_of(i);
-    if (i < tile1) {
-      load_k(i, pages);
-      load_v(i, pages);
-    }
-    int pages_next = pages_of(i + W);
-    for (; i < tile1; i += W) {
+    for (int i = tile0 + gw; i < tile1 && ok_all; i += GW) {
+      const uint32_t ok = have & ((1u << NS) - 1);
+      have >>= NS;
+      const uint32_t kb = my_k + (got % ST) * S::kStage, vb = my_v + (got % ST) * S::kStage;
+      wait(got, false);
       // ------------------------------------------------ scores
       float s[NS][NT][4];
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[u][n][c] = 0.0f;
+        Chunk<D / 8> k0, k1;
+        k0.load(kb + (16 * u + tok_g) * (D / 2) + t * (D / 8));
+        k1.load(kb + (16 * u + tok_g + 8) * (D / 2) + t * (D / 8));
+        Scales<NB> s0, s1;
+        s0.load(kb + S::kCodes + (16 * u + tok_g) * (2 * NB));
+        s1.load(kb + S::kCodes + (16 * u + tok_g + 8) * (2 * NB));
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
           float acc[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[n][c] = 0.0f;
+          bool first = true;
 #pragma unroll
           for (int st = 0; st < KS; ++st) {
             // k-step st: bytes 2 st and 2 st + 1 of the lane's two strips
             if (((st % (KS / 2)) * 4) / SW != blk) continue;
-            const uint32_t w0 = cur.k[u][0].w[st / 2], w1 = cur.k[u][1].w[st / 2];
-            uint32_t a0, a1, a2, a3;
+            const uint32_t w0 = k0.w[st / 2], w1 = k1.w[st / 2];
+            uint32_t x0, x1, x2, x3;  // table addresses
             if (st % 2 == 0) {
-              a0 = pair_of<0>(w0, lane_base), a1 = pair_of<0>(w1, lane_base);
-              a2 = pair_of<1>(w0, lane_base), a3 = pair_of<1>(w1, lane_base);
+              x0 = entry_of<0>(w0, lane_base), x1 = entry_of<0>(w1, lane_base);
+              x2 = entry_of<1>(w0, lane_base), x3 = entry_of<1>(w1, lane_base);
             } else {
-              a0 = pair_of<2>(w0, lane_base), a1 = pair_of<2>(w1, lane_base);
-              a2 = pair_of<3>(w0, lane_base), a3 = pair_of<3>(w1, lane_base);
+              x0 = entry_of<2>(w0, lane_base), x1 = entry_of<2>(w1, lane_base);
+              x2 = entry_of<3>(w0, lane_base), x3 = entry_of<3>(w1, lane_base);
             }
+            const uint32_t a0 = pair_at<0>(x0), a1 = pair_at<0>(x1), a2 = pair_at<0>(x2),
+                           a3 = pair_at<0>(x3);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_f16(acc[n], a0, a1, a2, a3, qf[n][st][0], qf[n][st][1]);
+            for (int n = 0; n < NT; ++n) {
+              if (first)
+                mma_f16_zero(acc[n], a0, a1, a2, a3, qf[n][st][0], qf[n][st][1]);
+              else
+                mma_f16(acc[n], a0, a1, a2, a3, qf[n][st][0], qf[n][st][1]);
+            }
+            if constexpr (KR) {
+              const uint32_t r0 = pair_at<128>(x0), r1 = pair_at<128>(x1), r2 = pair_at<128>(x2),
+                             r3 = pair_at<128>(x3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16(acc[n], r0, r1, r2, r3, qf[n][st][0], qf[n][st][1]);
+            }
+            first = false;
           }
           // an infinite scale would make every product infinite or NaN; its
           // row's score is NaN
-          float k0 = scale_at<F, NB>(cur.ka[u][0], blk), k1 = scale_at<F, NB>(cur.ka[u][1], blk);
-          k0 += k0 - k0;
-          k1 += k1 - k1;
+          float f0 = s0.template at<F>(blk), f1 = s1.template at<F>(blk);
+          f0 += f0 - f0;
+          f1 += f1 - f1;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            s[u][n][0] = fmaf(acc[n][0], k0, s[u][n][0]);
-            s[u][n][1] = fmaf(acc[n][1], k0, s[u][n][1]);
-            s[u][n][2] = fmaf(acc[n][2], k1, s[u][n][2]);
-            s[u][n][3] = fmaf(acc[n][3], k1, s[u][n][3]);
+            s[u][n][0] = blk ? fmaf(acc[n][0], f0, s[u][n][0]) : acc[n][0] * f0;
+            s[u][n][1] = blk ? fmaf(acc[n][1], f0, s[u][n][1]) : acc[n][1] * f0;
+            s[u][n][2] = blk ? fmaf(acc[n][2], f1, s[u][n][2]) : acc[n][2] * f1;
+            s[u][n][3] = blk ? fmaf(acc[n][3], f1, s[u][n][3]) : acc[n][3] * f1;
           }
         }
       }
-      const uint32_t ok = ok_k;
       // the next tile's keys are on their way while this one's weights form
-      if (i + W < tile1) load_k(i + W, pages_next);
+      const bool more = i + ST * GW < tile1;
+      if (more) have |= issue(i + ST * GW, pages_next, put, false) << (NS * (ST - 1));
 
       const int j0 = sp.base + i * TILE;
       const bool masked =
           ok != (1u << NS) - 1 || j0 < all_lo || j0 + TILE - 1 > all_hi;  // warp-uniform
-      float av[NS][2][NB];
-#pragma unroll
-      for (int u = 0; u < NS; ++u)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int blk = 0; blk < NB; ++blk) av[u][x][blk] = scale_at<F, NB>(cur.va[u][x], blk);
-      float top[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) top[n][0] = m[n][0], top[n][1] = m[n][1];
-#pragma unroll
-      for (int u = 0; u < NS; ++u)
+      if (masked) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v = s[u][n][c] * qs[n][c & 1];
-            if (masked) {
-              const int j = j0 + 16 * u + tok_g + 8 * (c >> 1);
-              if (!((ok >> u) & 1u) || j > see_hi[n][c & 1] || j < see_lo[n][c & 1]) v = -INFINITY;
-            }
-            s[u][n][c] = v;
-            top[n][c & 1] = fmaxf(top[n][c & 1], v);
-          }
-      if (masked) {  // scales of tokens that no row sees may be anything
+          for (int c = 0; c < 2; ++c) {
+            // last (inclusive) and first token that column 2 t + c sees
+            const int r = 8 * n + 2 * t + c;
+            const int pos = sp.first + (sp.r0 + r) / a.group;
+            const int hi = r >= sp.rows ? -1 : a.causal && pos < sp.len ? pos : sp.len - 1;
+            const int lo = a.window > 0 ? pos - a.window + 1 : 0;
 #pragma unroll
-        for (int u = 0; u < NS; ++u)
+            for (int u = 0; u < NS; ++u)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-          {
-            const int j = j0 + 16 * u + tok_g + 8 * x;
-            if (!((ok >> u) & 1u) || j >= sp.end || j < sp.lo)
-#pragma unroll
-              for (int blk = 0; blk < NB; ++blk) av[u][x][blk] = 0.0f;
+              for (int x = 0; x < 2; ++x) {
+                const int j = j0 + 16 * u + tok_g + 8 * x;
+                if (!((ok >> u) & 1u) || j > hi || j < lo) s[u][n][c + 2 * x] = -INFINITY;
+              }
           }
       }
+      float top[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          float x = -INFINITY;
 #pragma unroll
-          for (int x = 4; x <= 16; x <<= 1)
-            top[n][c] = fmaxf(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], x));
+          for (int u = 0; u < NS; ++u) x = fmaxf(x, fmaxf(s[u][n][c], s[u][n][c + 2]));
+#pragma unroll
+          for (int y = 4; y <= 16; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+          top[n][c] = fmaxf(m[n][c], x * qs[n][c]);  // qs > 0 (or NaN, which m ignores)
+        }
+      wait(got, true);
+      Scales<NB> vs[NS][2];
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          vs[u][x].load(vb + S::kCodes + (16 * u + tok_g + 8 * x) * (2 * NB));
+          if (masked) {  // scales of tokens that no row sees may be anything
+            const int j = j0 + 16 * u + tok_g + 8 * x;
+            if (!((ok >> u) & 1u) || j >= sp.end || j < sp.lo)
+#pragma unroll
+              for (int y = 0; y < (NB + 1) / 2; ++y) vs[u][x].w[y] = 0u;
+          }
+        }
       // running exponents of the value scales, and the factor that brings a
-      // weight times its scale to at most 2^15
-      float vn[NB];
-      bool grew = false;
-      float vgrow[NB];
+      // weight times its scale to at most 2^15 (infinite scales stay infinite)
+      float vn[NB], vgrow[NB];
+      bool up = false;
+      constexpr uint32_t kInf = F == BNB4_BF16 ? 0x7f80u : 0x7c00u;
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk) {
         uint32_t x = 0;
@@ -619,23 +706,22 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
         for (int u = 0; u < NS; ++u)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint32_t bits = __float_as_uint(av[u][y][blk]);
-            x = max(x, bits < 0x7f800000u ? bits : 0u);  // infinite ones stay infinite
+            const uint32_t w = vs[u][y].w[blk / 2];
+            const uint32_t bits = (blk & 1) ? w >> 16 : w & 0xffffu;
+            x = max(x, bits < kInf ? bits : 0u);
           }
         x = __reduce_max_sync(0xffffffffu, x);
-        const int e = static_cast<int>(x >> 23) - 127;
+        const int e =
+            F == BNB4_BF16 ? static_cast<int>(x >> 7) - 127 : static_cast<int>(x >> 10) - 15;
         vgrow[blk] = 1.0f;
         if (e > ve[blk]) {
           const int d = ve[blk] - e;
           vgrow[blk] = d < -126 ? 0.0f : pow2(d);
           ve[blk] = e;
-          grew = true;
+          up = true;
         }
         vn[blk] = pow2(14 - ve[blk]);
-#pragma unroll
-        for (int u = 0; u < NS; ++u) av[u][0][blk] *= vn[blk], av[u][1][blk] *= vn[blk];
       }
-      bool up = grew;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -656,26 +742,34 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
             }
           }
       }
+      float ref[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ref[n][c] = m[n][c] == -INFINITY ? 0.0f : m[n][c];
       // ------------------------------------------------ weights and values
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
-        float p[NT][4];
+        Chunk<D / 16> v[4];  // the lane's strip of tokens 2 t, 2 t + 1 and 8 more of each
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float mm = m[n][c & 1];
-            p[n][c] = ex2(s[u][n][c] - (mm == -INFINITY ? 0.0f : mm));
-            l[n][c & 1] += p[n][c];
-          }
+        for (int c = 0; c < 4; ++c)
+          v[c].load(vb + (16 * u + ((2 * t + (c & 1)) ^ (t & 1)) + 8 * (c >> 1)) * (D / 2) +
+                    g * (D / 16));
         uint32_t pb[NB][NT][2], pl[NB][NT][2];
 #pragma unroll
-        for (int blk = 0; blk < NB; ++blk)
+        for (int n = 0; n < NT; ++n) {
+          float p[4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int c = 0; c < 4; ++c) {
+            p[c] = ex2(fmaf(s[u][n][c], qs[n][c & 1], -ref[n][c & 1]));
+            l[n][c & 1] += p[c];
+          }
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              float y0 = p[n][2 * x] * av[u][x][blk], y1 = p[n][2 * x + 1] * av[u][x][blk];
+              const float av = vs[u][x].template at<F>(blk) * vn[blk];
+              float y0 = p[2 * x] * av, y1 = p[2 * x + 1] * av;
               if (masked) {  // 0 * infinity of a token that another row sees
                 y0 = s[u][n][2 * x] == -INFINITY ? 0.0f : y0;
                 y1 = s[u][n][2 * x + 1] == -INFINITY ? 0.0f : y1;
@@ -686,12 +780,12 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
                 pl[blk][n][x] = transpose8x8(pack_f16x2(
                     y0 - half_to_f32<BNB4_F16>(hi & 0xffffu), y1 - half_to_f32<BNB4_F16>(hi >> 16)));
             }
+        }
 #pragma unroll
         for (int wd = 0; wd < D / 64; ++wd) {
-          // word wd of the lane's strip for its 4 tokens: bytes of the codes
-          // of two tokens (even values; odd values)
-          const uint32_t w0 = cur.v[u][0].w[wd], w1 = cur.v[u][1].w[wd];
-          const uint32_t w2 = cur.v[u][2].w[wd], w3 = cur.v[u][3].w[wd];
+          // word wd of the strip for the 4 tokens: bytes of the codes of two
+          // tokens (even values; odd values)
+          const uint32_t w0 = v[0].w[wd], w1 = v[1].w[wd], w2 = v[2].w[wd], w3 = v[3].w[wd];
           const uint32_t ev0 = (w0 & 0xf0f0f0f0u) | ((w1 >> 4) & 0x0f0f0f0fu);
           const uint32_t od0 = ((w0 << 4) & 0xf0f0f0f0u) | (w1 & 0x0f0f0f0fu);
           const uint32_t ev1 = (w2 & 0xf0f0f0f0u) | ((w3 >> 4) & 0x0f0f0f0fu);
@@ -715,12 +809,15 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
                 pair_of<3>(ev1, lane_base), pair_of<3>(od1, lane_base));
         }
       }
-      if (i + W < tile1) load_v(i + W, pages_next);
-      pages_next = pages_of(i + 2 * W);
+      ++got;
+      if (more) {
+        issue(i + ST * GW, pages_next, put, true);
+        ++put;
+      }
+      pages_next = page_of(i + (ST + 1) * GW);
     }
-
     // ---------------------------------------------------- join the warps
-    const int busy = tile1 - tile0 < W ? tile1 - tile0 : W;  // warps with a tile
+    const int busy = tile1 - tile0 < GW ? tile1 - tile0 : GW;  // warps with a tile
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -732,77 +829,118 @@ __global__ void __launch_bounds__(W * 32, 1) attn_decode_kernel(const DecodeArgs
           sm_l[warp][8 * n + 2 * t + c] = l[n][c];
         }
       }
-    __syncthreads();
-    if (threadIdx.x < RT) {
+    group_sync(grp, GW * 32);
+    if (gw == 0 && lane < RT) {
       float top = -INFINITY;
-      for (int w = 0; w < busy; ++w) top = fmaxf(top, sm_m[w][threadIdx.x]);
-      const float ref = top == -INFINITY ? 0.0f : top;
+      for (int w = 0; w < busy; ++w) top = fmaxf(top, sm_m[grp * GW + w][lane]);
+      const float r = top == -INFINITY ? 0.0f : top;
       float sum = 0.0f;
-      for (int w = 0; w < busy; ++w) sum += sm_l[w][threadIdx.x] * ex2(sm_m[w][threadIdx.x] - ref);
-      sm_max[threadIdx.x] = top;
-      sm_sum[threadIdx.x] = sum;
+      for (int w = 0; w < busy; ++w) sum += sm_l[grp * GW + w][lane] * ex2(sm_m[grp * GW + w][lane] - r);
+      sm_max[grp][lane] = top;
+      sm_sum[grp][lane] = sum;
     }
-    __syncthreads();
     const float cinv = a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale;
-    const uint32_t mine = kJoinAt + static_cast<uint32_t>(warp) * (RT * D * 4);
-    if (warp < busy) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        // every warp finds the common maximum for its own columns
+        float top = -INFINITY;
+        for (int w = 0; w < busy; ++w) top = fmaxf(top, sm_m[grp * GW + w][8 * n + 2 * t + c]);
+        const float f = ex2(m[n][c] - (top == -INFINITY ? 0.0f : top)) * cinv;
+#pragma unroll
+        for (int x = 0; x < KS; ++x) {
+          const float back = pow2(ve[(2 * x) / SW] - 14);
+          o[x][n][c] = o[x][n][c] * f * back;
+          o[x][n][c + 2] = o[x][n][c + 2] * f * back;
+        }
+      }
+    // the upper ones of the warps that still hold sums hand them over, until warp 0 has them all: a fixed order
+    int live = busy;
+    while (live > 1) {
+      const int give = live / 2 < S::kGive ? live / 2 : S::kGive;
+      const int keep = live - give;  // warps keep .. live - 1 give to 0 ..
+      if (gw >= keep && gw < live) {
+#pragma unroll
+        for (int x = 0; x < KS; ++x)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                               S::piece(grp, ((gw - keep) * KS + x) * NT * 4 + n * 4 + c) + 4u * lane),
+                           "f"(o[x][n][c])
+                           : "memory");
+      }
+      group_sync(grp, GW * 32);
+      if (gw < give) {
+#pragma unroll
+        for (int x = 0; x < KS; ++x)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float y;
+              asm volatile("ld.shared.f32 %0, [%1];"
+                           : "=f"(y)
+                           : "r"(S::piece(grp, (gw * KS + x) * NT * 4 + n * 4 + c) + 4u * lane));
+              o[x][n][c] += y;
+            }
+      }
+      group_sync(grp, GW * 32);
+      live = keep;
+    }
+    const bool whole = tile0 == 0 && tile1 == sp.tiles;
+    if (gw == 0) {
+      __syncwarp();
+      // partial results: slot 0 continues the run before, slot 1 goes on in the next
+      float* part = a.ws + (static_cast<int64_t>(run) * 2 + (tile0 == 0 ? 1 : 0)) *
+                               (RT * D + 2 * RT);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int r = 8 * n + 2 * t + c;
-          const float top = sm_max[r];
-          const float f = ex2(m[n][c] - (top == -INFINITY ? 0.0f : top)) * cinv;
+          if (r < sp.rows) {
+            const float top = sm_max[grp][r], sum = sm_sum[grp][r];
+            if (whole) {
+              // SW values of each block, two at a time
+              const RowOut<F> out(a, sp, h, sp.r0 + r, top, sum, g == 0);
 #pragma unroll
-          for (int x = 0; x < KS; ++x) {
-            const int blk = (2 * x) / SW;
-            const int d = blk * BS + g * SW + (2 * x) % SW;
-            const float back = pow2(ve[blk] - 14);
-            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(mine + 4u * (r * D + d)),
-                         "f"(o[x][n][c] * f * back), "f"(o[x][n][c + 2] * f * back)
-                         : "memory");
+              for (int x = 0; x < KS; ++x)
+                out.pair((2 * x / SW) * BS + g * SW + (2 * x) % SW, o[x][n][c], o[x][n][c + 2]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < KS; ++x)
+                *reinterpret_cast<float2*>(part + r * D + (2 * x / SW) * BS + g * SW +
+                                           (2 * x) % SW) = make_float2(o[x][n][c], o[x][n][c + 2]);
+              if (g == 0) {
+                part[RT * D + r] = top;
+                part[RT * D + RT + r] = sum;
+              }
+            }
           }
         }
     }
-    __syncthreads();
-    const bool whole = tile0 == 0 && tile1 == sp.tiles;
-    // partial results: slot 0 continues the run before, slot 1 goes on in the next
-    float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (tile0 == 0 ? 1 : 0)) *
-                             (RT * D + 2 * RT);
-    for (int e = threadIdx.x; e < sp.rows * (D / 4); e += W * 32) {
-      const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < busy; ++w) {
-        float4 y;
-        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                     : "r"(kJoinAt + 4u * ((w * RT + r) * D + d)));
-        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-      }
-      if (whole) {
-        store_row<F>(a, sp, h, sp.r0 + r, d, v, sm_max[r], sm_sum[r]);
-      } else {
-        *reinterpret_cast<float4*>(part + r * D + d) = v;
-        if (d == 0) {
-          part[RT * D + r] = sm_max[r];
-          part[RT * D + RT + r] = sm_sum[r];
-        }
-      }
-    }
-    __syncthreads();  // the shared arrays are free for the next segment
+    group_sync(grp, GW * 32);  // the shared arrays are free for the next segment
     if (a.split) {
       left -= tile1 - tile0;
       tile0 = 0;
       if (++h == a.heads) h = 0, ++b;
     }
   }
+  // a wait that gave up: copies in flight land before the CTA ends
+  if (!ok_all)
+    for (uint32_t n = got; n < put + 1; ++n)
+      for (int v = 0; v < 2; ++v)
+        wait_drain(smem_u32(&bars[warp][(v ? ST : 0) + n % ST]), (n / ST) & 1, &ctl);
 }
 
 // Joins the partial results of the pairs that several runs share: CTA i takes
 // the pair that begins in run i and goes on in run i + 1.
-template <int D, int F, int NT, int NS>
+template <int D, int F, int NT, int TILE>
 __global__ void __launch_bounds__(256) attn_join_kernel(const DecodeArgs a) {
-  constexpr int RT = 8 * NT, TILE = 16 * NS;
+  constexpr int RT = 8 * NT;
   __shared__ int sm_item[5];
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -874,33 +1012,46 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const DecodeArgs a) {
       v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y);
       v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
     }
-    store_row<F>(a, sp, h, r, d, v, top, sum);
+    const RowOut<F> out(a, sp, h, r, top, sum, d == 0);
+    out.pair(d, v.x, v.y);
+    out.pair(d + 2, v.z, v.w);
   }
 }
 
 // ------------------------------------------------------------------- host
-constexpr int kMaxRuns = 192;  // bound of the grid, hence of the workspace
+constexpr int kMaxRuns = 320;  // bound of the runs, hence of the workspace
 
-template <int NT>
-constexpr int warps_of() { return NT == 1 ? 16 : 12; }
-constexpr int kSub = 2;  // 16-token sub-tiles per warp tile
-
-template <int D, int BS, int F, int NT>
-cudaError_t launch_t(const DecodeArgs& a, int grid, cudaStream_t s) {
-  constexpr int W = warps_of<NT>(), RT = 8 * NT;
-  constexpr int kSmem = static_cast<int>(kJoinAt) + W * RT * D * 4;
-  auto kern = attn_decode_kernel<D, BS, F, NT, kSub, W>;
+template <int D, int BS, int F, int NT, bool KR>
+cudaError_t launch_t(DecodeArgs& a, int64_t span, int num_sms, cudaStream_t s) {
+  using S = Shape<D, BS, F, NT, KR>;
+  // The arrays' shared addresses are fixed: everything from the first byte of
+  // shared memory to kEnd must be there (static and reserved bytes come off).
+  constexpr int kSmem = static_cast<int>(S::kEnd);
+  static_assert(kSmem + 4096 <= 232448, "shared memory budget");
+  // Whole pairs in turn where no pair has more than a tile per warp (a cut
+  // would only add the join), else the line of tiles cut into equal runs.
+  a.split = a.row_tiles == 1 && span > S::TILE * S::GW;
+  const int64_t items = static_cast<int64_t>(a.batch) * a.heads * a.row_tiles;
+  const int sms = num_sms < kMaxRuns / 2 ? num_sms : kMaxRuns / 2;
+  const int grid = a.split || items > 2 * sms ? sms : static_cast<int>((items + 1) / 2);
+  auto kern = attn_decode_kernel<D, BS, F, NT, KR>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(kern, dim3(grid), dim3(W * 32), kSmem, s, programmatic_after_kernel(s), a);
+  e = launch_kernel(kern, dim3(grid), dim3(S::W * 32), kSmem, s, programmatic_after_kernel(s), a);
   if (e != cudaSuccess || !a.split) return e;
-  return launch_kernel(attn_join_kernel<D, F, NT, kSub>, dim3(grid), dim3(256), 0, s, true, a);
+  return launch_kernel(attn_join_kernel<D, F, NT, S::TILE>, dim3(2 * grid), dim3(256), 0, s, true,
+                       a);
 }
 
 template <int D, int BS, int F>
-cudaError_t launch_f(const DecodeArgs& a, int rows, int grid, cudaStream_t s) {
-  return rows <= 8 ? launch_t<D, BS, F, 1>(a, grid, s) : launch_t<D, BS, F, 2>(a, grid, s);
+cudaError_t launch_f(DecodeArgs& a, int rows, int64_t span, int num_sms, cudaStream_t s) {
+  if constexpr (F == BNB4_F16)
+    if (a.qtype == kQtNF4)
+      return rows <= 8 ? launch_t<D, BS, F, 1, true>(a, span, num_sms, s)
+                       : launch_t<D, BS, F, 2, true>(a, span, num_sms, s);
+  return rows <= 8 ? launch_t<D, BS, F, 1, false>(a, span, num_sms, s)
+                   : launch_t<D, BS, F, 2, false>(a, span, num_sms, s);
 }
 
 }  // namespace
@@ -937,20 +1088,13 @@ cudaError_t launch_attn(const bnb4_attn& p, int num_sms, int* err, cudaStream_t 
   a.err = err;
   const int64_t rows = static_cast<int64_t>(a.max_q) * a.group;
   const int rt = rows <= 8 ? 8 : 16;
-  const int warps = rows <= 8 ? warps_of<1>() : warps_of<2>();
   a.row_tiles = static_cast<int>((rows + rt - 1) / rt);
-  // Whole pairs in turn where no pair has more than a tile per warp (a cut
-  // would only add the join), else the line of tiles cut into equal runs.
   const int64_t span = a.window > 0 && static_cast<int64_t>(a.window) + a.max_q + 15 < p.max_seq_len
                            ? a.window + a.max_q + 15
                            : p.max_seq_len;
-  a.split = a.row_tiles == 1 && span > 16 * kSub * warps;
-  const int64_t items = static_cast<int64_t>(a.batch) * a.heads * a.row_tiles;
-  const int sms = num_sms < kMaxRuns ? num_sms : kMaxRuns;
-  const int grid = a.split || items > sms ? sms : static_cast<int>(items);
-#define BNB4_ATTN(DV, BSV)                                                             \
-  return c.dtype == BNB4_F16 ? launch_f<DV, BSV, BNB4_F16>(a, rt, grid, s)             \
-                             : launch_f<DV, BSV, BNB4_BF16>(a, rt, grid, s);
+#define BNB4_ATTN(DV, BSV)                                                               \
+  return c.dtype == BNB4_F16 ? launch_f<DV, BSV, BNB4_F16>(a, rt, span, num_sms, s)      \
+                             : launch_f<DV, BSV, BNB4_BF16>(a, rt, span, num_sms, s);
   if (c.head_dim == 128) {
     if (c.blocksize == 128) { BNB4_ATTN(128, 128) }
     if (c.blocksize == 64) { BNB4_ATTN(128, 64) }

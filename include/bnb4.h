@@ -494,7 +494,7 @@ typedef struct bnb4_attn {
   int32_t block_table_width;
   int32_t causal;  /* 0 or 1 */
   int32_t window;  /* 0: none */
-  float scale;     /* > 0 */
+  float scale;     /* 1e-8 .. 1e8 */
   int32_t reserved; /* must be 0 */
 } bnb4_attn;
 
