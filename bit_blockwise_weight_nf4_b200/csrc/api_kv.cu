@@ -124,7 +124,12 @@ static int check_attn(const bnb4_attn* a) {
   if (static_cast<int64_t>(a->max_q_len) * a->n_heads > INT32_MAX) return BNB4_ERR_SHAPE;
   if (!a->cu_seqlens_q && static_cast<int64_t>(a->batch) * a->max_q_len != a->total_q)
     return BNB4_ERR_SHAPE;
-  if (a->block_table_width < 1 || a->block_table_stride < a->block_table_width)
+  if (a->block_table_width < 1 || a->block_table_stride < a->block_table_width ||
+      a->block_table_width > (1 << 30) / a->cache->page_size)
+    return BNB4_ERR_SHAPE;
+  // tiles of 16 rows and more, counted in 32 bits
+  if (static_cast<int64_t>(a->batch) * a->n_heads > (1 << 24) ||
+      static_cast<int64_t>(a->batch) * a->n_heads * (a->max_q_len / 64 + 1) > (1 << 30))
     return BNB4_ERR_SHAPE;
   if (!(a->scale >= 1e-8f && a->scale <= 1e8f)) return BNB4_ERR_INVALID_ARG;
   return BNB4_OK;

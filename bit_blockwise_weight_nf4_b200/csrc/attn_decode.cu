@@ -41,6 +41,7 @@
 //    pair may be shared with its neighbours, whose partial results (fp32, in
 //    the workspace) a second kernel joins in the order of the tokens, so
 //    results repeat bit for bit.
+#include "attn.cuh"
 #include "common.cuh"
 #include "kvcache.h"
 #include "kernels.h"
@@ -48,78 +49,6 @@
 
 namespace bnb4 {
 namespace {
-
-struct DecodeArgs {
-  const uint16_t* q;
-  uint16_t* out;
-  float* lse;
-  int64_t q_ts, q_hs, o_ts, o_hs;
-  const uint8_t *k_codes, *v_codes;
-  const uint16_t *k_absmax, *v_absmax;
-  const int32_t* block_table;
-  int64_t bt_stride;
-  const int32_t *seq_lens, *cu_q;
-  int64_t total_q;
-  int batch, heads, group, max_q, num_pages, bt_width, causal, window, qtype;
-  int row_tiles;  // row tiles per (sequence, head); > 1 only without `split`
-  int split;      // the line of tiles is cut into equal runs
-  FastDiv page;
-  float scale_log2;  // softmax scale * log2(e)
-  float* ws;
-  int* err;
-};
-
-// ------------------------------------------------------------ sequences
-// One row tile of one sequence: its rows, and the tokens any of them sees.
-struct Span {
-  int q0, n, rows, r0;  // first query row of the sequence, its queries, this tile's rows
-  int len, first;       // cached tokens; position of query 0
-  int lo, base, end, tiles;  // first token seen, the same rounded down to 16, end
-};
-
-template <int RT, int TILE>
-__device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, int rt) {
-  Span s;
-  if (a.cu_q) {
-    const int64_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
-    const int64_t c = lo < 0 ? 0 : lo > a.total_q ? a.total_q : lo;
-    const int64_t e = hi < c ? c : hi > a.total_q ? a.total_q : hi;
-    s.q0 = static_cast<int>(c);
-    s.n = static_cast<int>(e - c);
-  } else {
-    s.q0 = b * a.max_q;
-    s.n = a.max_q;
-  }
-  const int64_t room = static_cast<int64_t>(a.bt_width) * a.page.d;
-  int len = a.seq_lens[b];
-  len = len < 0 ? 0 : len;
-  s.len = len > room ? static_cast<int>(room) : len;
-  s.first = s.len - s.n;
-  const int n = s.n < a.max_q ? s.n : a.max_q;  // rows past max_q are not computed
-  s.r0 = rt * RT;
-  int rows = n * a.group - s.r0;
-  s.rows = rows < 0 ? 0 : rows > RT ? RT : rows;
-  s.lo = s.base = s.end = s.tiles = 0;
-  if (s.rows > 0) {
-    const int i0 = s.r0 / a.group, i1 = (s.r0 + s.rows - 1) / a.group;
-    const int last = s.first + i1;  // position of the last row
-    s.end = a.causal && last + 1 < s.len ? last + 1 : s.len;
-    if (s.end < 0) s.end = 0;
-    int lo = a.window > 0 ? s.first + i0 - a.window + 1 : 0;
-    if (lo < 0) lo = 0;
-    s.lo = lo;
-    s.base = lo & ~15;
-    // at least one tile, so that rows that see nothing are still written
-    s.tiles = s.end > s.base ? (s.end - s.base + TILE - 1) / TILE : 1;
-  }
-  return s;
-}
-
-__device__ __forceinline__ int64_t warp_sum(int64_t x) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 
 // ------------------------------------------------------------ primitives
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -141,19 +70,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^e for -126 <= e <= 127
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
-
 constexpr uint32_t kTilesAt = 0x1000;   // shared address behind the static arrays
 constexpr uint32_t kTableAt = 0x10000;  // and of the pair table
 
@@ -177,14 +93,6 @@ template <int I>
 __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_base) {
   return pair_at<0>(entry_of<I>(w, lane_base));
 }
-
-// The code table times this constant rounds to fp16 within 3.1e-4 of a value,
-// exactly at the block's largest (1 and -1), with a root mean square error of
-// 3.6e-5 of the scale (as it stands: 7e-5); of the constants with exact ends
-// it leaves the least error in attention over normal keys (simulated: 2.0e-4
-// of the output against 4.3e-4).  FP4's magnitudes times 6 are E2M1's, exact.
-constexpr float kNf4Scale = 1613.0f / 1024.0f;
-constexpr float kFp4Scale = 6.0f;
 
 // KR: the second 128 bytes of an entry hold what the first rounded away.
 template <bool KR>
@@ -260,31 +168,6 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
 }
 
-// Where row r of (sequence, key/value head) goes, divided by its sum of weights
-// (relative to 2^top).  A row that saw no token has top = -infinity and sum 0
-// (a NaN score leaves a NaN sum) and gives zeros.
-template <int F>
-struct RowOut {
-  uint16_t* at;
-  float inv;
-  bool sees;
-  __device__ __forceinline__ RowOut(const DecodeArgs& a, const Span& sp, int h, int r, float top,
-                                    float sum, bool write_lse) {
-    const int i = r / a.group, hh = r - i * a.group;
-    const int64_t tok = static_cast<int64_t>(sp.q0) + i;
-    const int head = h * a.group + hh;
-    sees = top != -INFINITY || sum != 0.0f;
-    inv = 1.0f / sum;
-    at = a.out + tok * a.o_ts + head * a.o_hs;
-    if (write_lse && a.lse)
-      a.lse[tok * (static_cast<int64_t>(a.heads) * a.group) + head] =
-          sees ? (top + lg2(sum)) * 0.693147180559945f : -INFINITY;
-  }
-  __device__ __forceinline__ void pair(int d, float x, float y) const {
-    *reinterpret_cast<uint32_t*>(at + d) = sees ? pack2<F>(x * inv, y * inv) : 0u;
-  }
-};
-
 // ------------------------------------------------------------- the kernel
 // D, BS: head dimension and block size.  F: the 16-bit type.  NT: 8-row
 // groups of the row tile.  KR: the keys' table entries keep their rounding
@@ -329,7 +212,7 @@ struct Ctl {  // the fields that a bounded wait looks at
 
 template <int D, int BS, int F, int NT, bool KR>
 __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
-    attn_decode_kernel(const DecodeArgs a) {
+    attn_decode_kernel(const AttnArgs a) {
   using S = Shape<D, BS, F, NT, KR>;
   constexpr int NS = S::NS, ST = S::ST, W = S::W, GW = S::GW, RT = S::RT, TILE = S::TILE;
   constexpr int NB = S::NB, KS = S::KS;
@@ -939,7 +822,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
 // Joins the partial results of the pairs that several runs share: CTA i takes
 // the pair that begins in run i and goes on in run i + 1.
 template <int D, int F, int NT, int TILE>
-__global__ void __launch_bounds__(256) attn_join_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   constexpr int RT = 8 * NT;
   __shared__ int sm_item[5];
   pdl_wait();
@@ -1022,7 +905,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const DecodeArgs a) {
 constexpr int kMaxRuns = 320;  // bound of the runs, hence of the workspace
 
 template <int D, int BS, int F, int NT, bool KR>
-cudaError_t launch_t(DecodeArgs& a, int64_t span, int num_sms, cudaStream_t s) {
+cudaError_t launch_t(AttnArgs& a, int64_t span, int num_sms, cudaStream_t s) {
   using S = Shape<D, BS, F, NT, KR>;
   // The arrays' shared addresses are fixed: everything from the first byte of
   // shared memory to kEnd must be there (static and reserved bytes come off).
@@ -1045,7 +928,7 @@ cudaError_t launch_t(DecodeArgs& a, int64_t span, int num_sms, cudaStream_t s) {
 }
 
 template <int D, int BS, int F>
-cudaError_t launch_f(DecodeArgs& a, int rows, int64_t span, int num_sms, cudaStream_t s) {
+cudaError_t launch_f(AttnArgs& a, int rows, int64_t span, int num_sms, cudaStream_t s) {
   if constexpr (F == BNB4_F16)
     if (a.qtype == kQtNF4)
       return rows <= 8 ? launch_t<D, BS, F, 1, true>(a, span, num_sms, s)
@@ -1056,16 +939,16 @@ cudaError_t launch_f(DecodeArgs& a, int rows, int64_t span, int num_sms, cudaStr
 
 }  // namespace
 
-size_t attn_workspace_bytes(const bnb4_attn& a) {
-  const int64_t rows = static_cast<int64_t>(a.max_q_len) * (a.n_heads / a.cache->n_kv_heads);
-  if (rows > 16) return 0;
-  const size_t rt = rows <= 8 ? 8 : 16;
-  return sizeof(float) * 2 * kMaxRuns * rt * (static_cast<size_t>(a.cache->head_dim) + 2);
-}
+// At most this many rows per (sequence, key/value head) run here; more go to
+// the tensor-core kernel.
+constexpr int64_t kMaxRows = 16;
+// The workspace query knows no device: it splits for this many SMs, and so
+// does the launch.
+constexpr int kSms = 148;
 
-cudaError_t launch_attn(const bnb4_attn& p, int num_sms, int* err, cudaStream_t s) {
+static AttnArgs args_of(const bnb4_attn& p, int64_t* rows, int64_t* span) {
   const bnb4_kv_cache& c = *p.cache;
-  DecodeArgs a = {};
+  AttnArgs a = {};
   a.q = static_cast<const uint16_t*>(p.q);
   a.out = static_cast<uint16_t*>(p.out);
   a.lse = p.lse;
@@ -1081,17 +964,34 @@ cudaError_t launch_attn(const bnb4_attn& p, int num_sms, int* err, cudaStream_t 
   a.max_q = p.max_q_len;
   a.num_pages = static_cast<int>(c.num_pages);
   a.bt_width = p.block_table_width;
-  a.causal = p.causal, a.window = p.window, a.qtype = c.qtype;
+  a.causal = p.causal, a.qtype = c.qtype;
+  a.window = p.window < (1 << 30) ? p.window : 1 << 30;
   a.page = make_div(static_cast<uint32_t>(c.page_size));
   a.scale_log2 = p.scale * 1.44269504088896f;
   a.ws = static_cast<float*>(p.workspace);
+  *rows = static_cast<int64_t>(a.max_q) * a.group;
+  // tokens that a row tile sees at most (a wide one: its queries' too)
+  const int64_t own = *rows <= kMaxRows ? a.max_q : 256 / a.group + 2;
+  *span = a.window > 0 && a.window + own + 15 < p.max_seq_len ? a.window + own + 15 : p.max_seq_len;
+  return a;
+}
+
+size_t attn_workspace_bytes(const bnb4_attn& p) {
+  int64_t rows, span;
+  const AttnArgs a = args_of(p, &rows, &span);
+  if (rows > kMaxRows) return attn_prefill_workspace(a, p.cache->head_dim, rows, span, kSms);
+  const size_t rt = rows <= 8 ? 8 : 16;
+  return sizeof(float) * 2 * kMaxRuns * rt * (static_cast<size_t>(p.cache->head_dim) + 2);
+}
+
+cudaError_t launch_attn(const bnb4_attn& p, int num_sms, int* err, cudaStream_t s) {
+  const bnb4_kv_cache& c = *p.cache;
+  int64_t rows, span;
+  AttnArgs a = args_of(p, &rows, &span);
   a.err = err;
-  const int64_t rows = static_cast<int64_t>(a.max_q) * a.group;
+  if (rows > kMaxRows) return launch_attn_prefill(a, c, rows, span, kSms, s);
   const int rt = rows <= 8 ? 8 : 16;
-  a.row_tiles = static_cast<int>((rows + rt - 1) / rt);
-  const int64_t span = a.window > 0 && static_cast<int64_t>(a.window) + a.max_q + 15 < p.max_seq_len
-                           ? a.window + a.max_q + 15
-                           : p.max_seq_len;
+  a.row_tiles = 1;
 #define BNB4_ATTN(DV, BSV)                                                               \
   return c.dtype == BNB4_F16 ? launch_f<DV, BSV, BNB4_F16>(a, rt, span, num_sms, s)      \
                              : launch_f<DV, BSV, BNB4_BF16>(a, rt, span, num_sms, s);

@@ -1,0 +1,846 @@
+// attn_prefill.cu -- attention of many query rows over a paged 4-bit
+// key/value cache on sm_100a (chunks of prompts): the tier of bnb_attn_4bit
+// for more than 16 rows (queries x grouped heads) per key/value head.
+//
+// Two matrix products on the tensor cores (tcgen05, fp16 in, fp32 sums in
+// tensor memory) around an online softmax, for tiles of 2 x 128 rows against
+// 128 tokens; what bounds it is the instruction issue and the exponentials of
+// the softmax, next to which the cache's decode has to fit.
+//
+// Roles of a CTA's 17 warps (one CTA per SM):
+//  * warps 0-3 and 4-7: the softmax of row tile 0 and 1, one row per thread.
+//    Scores are read from tensor memory twice (their maximum; then the
+//    weights), 32 at a time, so a row never needs 128 registers.  The running
+//    maximum is only raised when it grows by more than 8 binades; until then
+//    weights exceed one, and the sums in tensor memory need no rescaling.
+//    The weights go back to tensor memory, over the scores, as the A operand
+//    of the second product.
+//  * warps 8-11: the keys.  Thread r owns token r of the tile: 64 codes a
+//    64-byte row in registers one tile ahead, looked up by byte permutes in
+//    the constant table, times the block's scale, into the swizzled K-major
+//    operand.
+//  * warps 12-15: the values.  Thread u owns 8 tokens x 8 values: its 8 words
+//    of codes are transposed nibble by nibble in registers (3 butterfly
+//    steps), so that the operand (values as rows, tokens as K) is again
+//    written 8 codes and 16 bytes at a time.
+//  * warp 16: tensor memory and the issue of both products; the two row tiles
+//    take turns, so one's products run under the other's softmax.
+// The stored order of a row's values is kept for K and q alike (a dot product
+// does not care) and undone when the output is written.
+//
+// Precision.  q as in the decode kernel; keys are rounded to fp16 after
+// scaling by the tile's largest scale's power of two -- an absolute error in
+// the scores --, values by a running power of two, to at most 2^16, and weights
+// by 2^7 (so at most 2^15): both stay normal 21 binades and more below the
+// largest.  Every mbarrier wait is bounded; no TMA load is used.
+#include "attn.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "kvcache.h"
+#include "lut.cuh"
+#include "sm100.cuh"
+
+namespace bnb4 {
+namespace {
+
+constexpr int TK = 128;        // tokens per tile
+constexpr int TR = 128;        // rows per row tile (threads of a softmax group)
+constexpr int kRowsCta = 2 * TR;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;
+constexpr int kThreads = 17 * 32;
+constexpr int kStages = 2;     // decoded tiles of keys, and of values
+constexpr int kRing = 4;       // tiles' scalars: see Meta
+constexpr float kLazy = 8.0f;  // growth of the maximum that is let pass, in binades
+constexpr int kBoost = 7;      // weights are held times 2^kBoost
+// Values are held times 2^(top - exponent of the largest scale): NF4's table
+// ends at 1.58, FP4's at 6, so at most 5.2e4 in fp16.
+__host__ __device__ constexpr int value_top(int qtype) { return qtype == kQtNF4 ? 14 : 12; }
+constexpr int kHalf = TK * 128;  // 128 rows of 128 bytes
+
+template <int D>
+struct Smem {
+  static constexpr int kQ = (D / 64) * kHalf;        // one row tile of q
+  static constexpr int kK = (D / 64) * kHalf;        // one tile of keys
+  static constexpr int kV = (TK / 64) * D * 128;     // one tile of values
+  static constexpr int kOffK = 2 * kQ;
+  static constexpr int kOffV = kOffK + kStages * kK;
+  static constexpr int kOffCtl = kOffV + kStages * kV;
+};
+
+// A tile's scalars, in a ring of 4: tile j + 4's are written after the scores
+// of tile j + 2 were asked for, hence after both row tiles' softmax of tile j
+// + 1 -- the last readers of tile j's are done, and a wait never falls two
+// phases behind.
+struct Meta {
+  int key_exp, value_exp;   // keys are held times 2^-key_exp, values 2^(top - value_exp)
+  uint8_t present[4];       // per key warp: bit s: its sub-tile s (16 tokens) is cached
+  uint32_t bad[4];          // tokens whose value scale is not finite
+};
+
+struct Ctl {
+  uint64_t q_full, s_full[2], p_full[2], o_full[2];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t m_full[kRing];
+  uint64_t wait_limit_ns;
+  uint32_t tmem_base;
+  int abort;
+  uint32_t top[2][4];  // the key and value warps' largest scales
+  Meta meta[kRing];
+};
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// the A operand in tensor memory
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t at, const float (&v)[32]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_done() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// The 4 warps of the keys (or the values) meet.
+__device__ __forceinline__ void group_sync(int id) {
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
+// The same, and whether all of them bring true: they leave their loop together.
+__device__ __forceinline__ bool group_all(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, %2, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// The table times its constant, in fp16, as two byte-split halves.
+__device__ __forceinline__ Lut make_table(int qtype) {
+  uint32_t P[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float n0 = __fmul_rn(nf4_value(2 * j), kNf4Scale);
+    const float n1 = __fmul_rn(nf4_value(2 * j + 1), kNf4Scale);
+    // E2M1's magnitudes, exact
+    constexpr float e[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
+    const float sgn = j >= 4 ? -1.0f : 1.0f;
+    P[j] = qtype == kQtNF4 ? pack_f16x2(n0, n1)
+                           : pack_f16x2(sgn * e[(2 * j) & 7], sgn * e[(2 * j + 1) & 7]);
+  }
+  Lut l;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    l.L[q] = prmt(P[2 * q], P[2 * q + 1], 0x6420);
+    l.H[q] = prmt(P[2 * q], P[2 * q + 1], 0x7531);
+  }
+  return l;
+}
+
+// 8 words of 8 codes (byte j = codes 2 j, 2 j + 1, the first in the high
+// nibble): word i's code k becomes word k's code i.
+__device__ __forceinline__ void transpose_codes(uint32_t (&w)[8]) {
+  // exchange halves at distance 4 words / 16 bits, 2 / 8, then nibbles
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i], b = w[i + 4];
+    w[i] = prmt(a, b, 0x5410);
+    w[i + 4] = prmt(a, b, 0x7632);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if ((i & 2) == 0) {
+      const uint32_t a = w[i], b = w[i + 2];
+      w[i] = prmt(a, b, 0x6240);
+      w[i + 2] = prmt(a, b, 0x7351);
+    }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t a = w[i], b = w[i + 1];
+    w[i] = (a & 0xf0f0f0f0u) | ((b >> 4) & 0x0f0f0f0fu);
+    w[i + 1] = ((a << 4) & 0xf0f0f0f0u) | (b & 0x0f0f0f0fu);
+  }
+}
+
+// Stored place x (a multiple of 4) of a row -> the value's number in the row.
+template <int D, int BS>
+__device__ __forceinline__ constexpr int value_at(int x) {
+  constexpr int w = BS / 8;
+  const int strip = x / (D / 8), y = x % (D / 8);
+  return (y / w) * BS + strip * w + y % w;
+}
+
+struct PrefillArgs {
+  AttnArgs a;
+  int splits;
+};
+
+template <int D, int BS, int F>
+__global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const PrefillArgs pa) {
+  using S = Smem<D>;
+  constexpr int NB = D / BS;
+  const AttnArgs& a = pa.a;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + S::kOffCtl);
+  __shared__ __align__(16) uint16_t value_scale[NB][TK];  // fp16, of the tile being decoded
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  pdl_wait();
+
+  // this CTA's rows (the tiles with the most tokens first) and tokens
+  const int pairs = a.batch * a.heads;
+  const int item = static_cast<int>(blockIdx.x) / pa.splits;
+  const int split = static_cast<int>(blockIdx.x) - item * pa.splits;
+  const int pair = item % pairs;
+  const int rt = a.row_tiles - 1 - item / pairs;
+  const int h = pair % a.heads, b = pair / a.heads;
+  const Span sp = span_of<kRowsCta, TK>(a, b, rt);
+  if (sp.rows == 0) return;  // uniform over the CTA
+  const int per = (sp.tiles + pa.splits - 1) / pa.splits;
+  const int tile0 = split * per < sp.tiles ? split * per : sp.tiles;
+  const int tile1 = tile0 + per < sp.tiles ? tile0 + per : sp.tiles;
+  const int T = tile1 - tile0;  // 0: nothing to add (a partial result of no weight)
+  const int nr = sp.rows > TR ? 2 : 1;
+  const int32_t* bt = a.block_table + static_cast<int64_t>(b) * a.bt_stride;
+  auto bar = [&](uint64_t& x) { return smem_u32(&x); };
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(ctl->q_full), 4 * nr);
+    for (int r = 0; r < 2; ++r) {
+      mbar_init(bar(ctl->s_full[r]), 1);
+      mbar_init(bar(ctl->p_full[r]), 4);
+      mbar_init(bar(ctl->o_full[r]), 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(ctl->k_full[s]), 4);
+      mbar_init(bar(ctl->k_empty[s]), 1);
+      mbar_init(bar(ctl->v_full[s]), 4);
+      mbar_init(bar(ctl->v_empty[s]), 1);
+    }
+    for (int s = 0; s < kRing; ++s) mbar_init(bar(ctl->m_full[s]), 8);
+    ctl->abort = 0;
+    ctl->wait_limit_ns = kWaitLimitNs;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&ctl->tmem_base)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = ctl->tmem_base;
+  // columns: scores (and weights over them) of row tile r at 128 r, sums at 256 + 128 r
+  auto s_col = [&](int r) { return tmem + 128u * r; };
+  auto o_col = [&](int r) { return tmem + 256u + 128u * r; };
+  // one decision per warp: lane 0 waits, the others follow
+  auto warp_wait = [&](uint64_t& x, uint32_t parity) {
+    bool w = true;
+    if (lane == 0) w = wait_bounded(bar(x), parity, ctl, a.err);
+    return __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
+  };
+
+  if (warp < kKeyWarp) {
+    // ------------------------------------------------------------ softmax
+    const int r = warp >> 2;
+    if (r < nr) {
+      const int row = static_cast<int>(threadIdx.x);  // of the CTA's 256
+      const int rr = sp.r0 + row;
+      const bool real = row < sp.rows;
+      const int i = real ? rr / a.group : 0, hh = real ? rr - i * a.group : 0;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      float qs = a.scale_log2;
+      {  // q, in the stored order, as fp16
+        const uint16_t* src = a.q + (static_cast<int64_t>(sp.q0) + i) * a.q_ts +
+                              (static_cast<int64_t>(h) * a.group + hh) * a.q_hs;
+        uint4 x[D / 8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          x[c] = make_uint4(0, 0, 0, 0);
+          if (real) {
+            if constexpr (BS >= 64) {
+              x[c] = __ldg(reinterpret_cast<const uint4*>(src + value_at<D, BS>(8 * c)));
+            } else {
+              const uint2 y0 = __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c)));
+              const uint2 y1 =
+                  __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c + 4)));
+              x[c] = make_uint4(y0.x, y0.y, y1.x, y1.y);
+            }
+          }
+          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            top = max(top, max(w[y] & 0x7fffu, (w[y] >> 16) & 0x7fffu));
+        }
+        float f = 1.0f;
+        if constexpr (F == BNB4_BF16) {
+          int e = static_cast<int>(top >> 7) - 127;
+          e = e < -100 ? -100 : e;
+          f = pow2(14 - e);
+          qs *= pow2(e - 14);
+        }
+        if (top >= (F == BNB4_BF16 ? 0x7f80u : 0x7c00u)) qs = __int_as_float(0x7fffffff);
+        qs *= a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale;
+        uint8_t* dst = smem + r * S::kQ + (row & (TR - 1)) * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 y = x[c];
+          if constexpr (F == BNB4_BF16)
+            y = make_uint4(pack_f16x2(bf16_lo(y.x) * f, bf16_hi(y.x) * f),
+                           pack_f16x2(bf16_lo(y.y) * f, bf16_hi(y.y) * f),
+                           pack_f16x2(bf16_lo(y.z) * f, bf16_hi(y.z) * f),
+                           pack_f16x2(bf16_lo(y.w) * f, bf16_hi(y.w) * f));
+          *reinterpret_cast<uint4*>(dst + (c / 8) * kHalf + (((c & 7) ^ (row & 7)) << 4)) = y;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ctl->q_full));
+      }
+      // what this row sees, and what all rows of the row tile see
+      const int pos = sp.first + rr / a.group;
+      const int see_hi = !real ? -1 : a.causal && pos < sp.len ? pos : sp.len - 1;
+      const int see_lo = a.window > 0 ? pos - a.window + 1 : 0;
+      const int last_row = sp.rows < TR * (r + 1) ? sp.rows - 1 : TR * (r + 1) - 1;
+      const int pos0 = sp.first + (sp.r0 + TR * r) / a.group;
+      const int all_hi = a.causal && pos0 < sp.len ? pos0 : sp.len - 1;
+      const int all_lo = a.window > 0 ? sp.first + (sp.r0 + last_row) / a.group - a.window + 1 : 0;
+
+      float m = -INFINITY, l = 0.0f;
+      int ve = 0;
+      bool ok = true;
+      for (int j = 0; j < T; ++j) {
+        if (!warp_wait(ctl->s_full[r], j & 1) || !warp_wait(ctl->m_full[j % kRing], (j / kRing) & 1)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const Meta& mt = ctl->meta[j % kRing];
+        const uint32_t present = *reinterpret_cast<const uint32_t*>(mt.present);
+        const int tve = mt.value_exp;
+        const float q2 = qs * pow2(mt.key_exp);
+        const int j0 = sp.base + (tile0 + j) * TK;
+        const bool masked =
+            present != 0x03030303u || j0 < all_lo || j0 + TK - 1 > all_hi;  // warp-uniform
+        // columns lo .. hi of the tile are inside what the row sees
+        const int lo = see_lo - j0, hi = see_hi - j0;
+        float v[32];
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < TK / 32; ++c) {
+          tmem_load32(s_col(r) + lanes + 32 * c, v);
+          if (masked) {
+            const uint32_t here = present >> (8 * c);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((here >> (x / 16)) & 1u) || 32 * c + x < lo || 32 * c + x > hi)
+                v[x] = -INFINITY;
+          }
+          float t0 = v[0], t1 = v[1];
+#pragma unroll
+          for (int x = 2; x < 32; x += 2) t0 = fmaxf(t0, v[x]), t1 = fmaxf(t1, v[x + 1]);
+          top = fmaxf(top, fmaxf(t0, t1));
+        }
+        top *= q2;  // q2 > 0, or NaN (which the comparisons below ignore)
+        const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
+        const bool shift = j > 0 && tve != ve;
+        if (__any_sync(0xffffffffu, grow) || shift) {
+          const float old = m;
+          if (grow) m = top;
+          float f = grow ? ex2(old - m) : 1.0f;
+          l *= f;
+          if (shift) f *= ve - tve < -126 ? 0.0f : pow2(ve - tve);
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_load32(o_col(r) + lanes + 32 * c, v);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) v[x] *= f;
+              tmem_store32(o_col(r) + lanes + 32 * c, v);
+            }
+          }
+        }
+        ve = tve;
+        const float ref = (m == -INFINITY ? 0.0f : m) - static_cast<float>(kBoost);
+        float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < TK / 32; ++c) {
+          tmem_load32(s_col(r) + lanes + 32 * c, v);
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = ex2(fmaf(v[x], q2, -ref));
+          if (masked) {
+            const uint32_t here = present >> (8 * c);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((here >> (x / 16)) & 1u) || 32 * c + x < lo || 32 * c + x > hi) v[x] = 0.0f;
+          }
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            l0 += v[2 * x];
+            l1 += v[2 * x + 1];
+            p[x] = pack_f16x2(v[2 * x], v[2 * x + 1]);
+          }
+          tmem_store16(s_col(r) + lanes + 16 * c, p);
+        }
+        l += l0 + l1;
+        // a value that is not finite, of a token that this row sees
+        if ((mt.bad[0] | mt.bad[1] | mt.bad[2] | mt.bad[3]) != 0)
+          for (int x = 0; x < TK; ++x)
+            if ((mt.bad[x >> 5] >> (x & 31)) & 1u)
+              if (x >= lo && x <= hi) l = __int_as_float(0x7fffffff);
+        tmem_store_done();
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ctl->p_full[r]));
+      }
+      // ---------------------------------------------------------- output
+      if (ok && T > 0) {
+        ok = warp_wait(ctl->o_full[r], 0);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      }
+      if (ok) {  // warp-uniform
+        const float back = pow2(ve - value_top(a.qtype)) *
+                           (a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale);
+        const float lse_top = m - static_cast<float>(kBoost);
+        const bool sees = m != -INFINITY || l != 0.0f;
+        float v[32];
+        if (pa.splits == 1) {
+          const float inv = back / l;
+          const int64_t tok = static_cast<int64_t>(sp.q0) + i;
+          const int head = h * a.group + hh;
+          uint16_t* dst = a.out + tok * a.o_ts + head * a.o_hs;
+          if (real && a.lse)
+            a.lse[tok * (static_cast<int64_t>(a.heads) * a.group) + head] =
+                sees ? (lse_top + lg2(l)) * 0.693147180559945f : -INFINITY;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_load32(o_col(r) + lanes + 32 * c, v);
+            if (real) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 8) {
+                uint4 w;
+                w.x = sees ? pack2<F>(v[x] * inv, v[x + 1] * inv) : 0u;
+                w.y = sees ? pack2<F>(v[x + 2] * inv, v[x + 3] * inv) : 0u;
+                w.z = sees ? pack2<F>(v[x + 4] * inv, v[x + 5] * inv) : 0u;
+                w.w = sees ? pack2<F>(v[x + 6] * inv, v[x + 7] * inv) : 0u;
+                if constexpr (BS >= 64) {
+                  *reinterpret_cast<uint4*>(dst + value_at<D, BS>(32 * c + x)) = w;
+                } else {
+                  *reinterpret_cast<uint2*>(dst + value_at<D, BS>(32 * c + x)) =
+                      make_uint2(w.x, w.y);
+                  *reinterpret_cast<uint2*>(dst + value_at<D, BS>(32 * c + x + 4)) =
+                      make_uint2(w.z, w.w);
+                }
+              }
+            }
+          }
+        } else {
+          // partial sums (in the stored order), then {maximum, sum} per row
+          float* part = a.ws + static_cast<int64_t>(blockIdx.x) * kRowsCta * (D + 2);
+          if (real) {
+            part[kRowsCta * D + 2 * row] = lse_top;
+            part[kRowsCta * D + 2 * row + 1] = l;
+          }
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            if (T > 0) {  // CTA-uniform
+              tmem_load32(o_col(r) + lanes + 32 * c, v);
+              if (real) {
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                  *reinterpret_cast<float4*>(part + row * D + 32 * c + x) =
+                      make_float4(v[x] * back, v[x + 1] * back, v[x + 2] * back, v[x + 3] * back);
+              }
+            }
+          }
+        }
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ------------------------------------------- keys and values: decode
+    const bool values = warp >= kValueWarp;
+    const int u = static_cast<int>(threadIdx.x) - (values ? kValueWarp : kKeyWarp) * 32;
+    const Lut lut = make_table(a.qtype);
+    // token u of the tile: its cache row, or -1
+    auto row_of = [&](int tile, int tok) {
+      int64_t row = -1;
+      const int j = sp.base + (tile0 + tile) * TK + tok;
+      // whole sub-tiles of 16 tokens are brought in (a page holds them whole)
+      if (tile < T && (j & ~15) < sp.end) {
+        const uint32_t x = a.page.div(static_cast<uint32_t>(j));
+        const int p = __ldg(bt + x);
+        if (p >= 0 && p < a.num_pages)
+          row = (static_cast<int64_t>(p) * a.heads + h) * a.page.d +
+                (static_cast<uint32_t>(j) - x * a.page.d);
+      }
+      return row;
+    };
+    // scales of token u: raw patterns
+    const uint16_t* absmax = values ? a.v_absmax : a.k_absmax;
+    auto load_scales = [&](int64_t row, uint32_t (&s)[NB]) {
+#pragma unroll
+      for (int x = 0; x < NB; ++x) s[x] = row >= 0 ? __ldg(absmax + row * NB + x) : 0u;
+    };
+    // codes: a key thread's whole token (D / 8 words); a value thread's words
+    // word0 .. of the 8 tokens of `group`.  8 neighbouring lanes take 8 groups,
+    // whose 16-byte pieces of an operand row fall into different banks.
+    constexpr int kWords = D / 8, kUnits = D / 64;
+    const int group = (lane & 7) + 8 * (warp & 1);
+    const int word0 = kUnits * ((lane >> 3) + 4 * ((warp >> 1) & 1));
+    uint32_t w[16], wn[16];
+    // rows of this tile's token, and of the next tile's: a key thread's token,
+    // a value thread's first of 8
+    int64_t row = row_of(0, u);
+    int64_t row1 = row_of(1, u), at1 = row_of(0, 8 * group);
+    auto load_codes = [&](uint32_t (&x)[16], int64_t at) {
+      if (!values) {
+#pragma unroll
+        for (int y = 0; y < kWords / 4; ++y) {
+          const uint4 c = at >= 0 ? ldg_stream_v4(a.k_codes + at * (D / 2) + 16 * y)
+                                  : make_uint4(0, 0, 0, 0);
+          x[4 * y] = c.x, x[4 * y + 1] = c.y, x[4 * y + 2] = c.z, x[4 * y + 3] = c.w;
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const uint8_t* src = a.v_codes + (at + y) * (D / 2) + 4 * word0;
+          if constexpr (kUnits == 2) {
+            const uint2 c =
+                at >= 0 ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
+            x[y] = c.x, x[8 + y] = c.y;
+          } else {
+            x[y] = at >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(src)) : 0u;
+          }
+        }
+      }
+    };
+    uint32_t sc[NB], scn[NB];
+    load_scales(row, sc);
+    load_codes(w, values ? at1 : row);
+    at1 = row_of(1, 8 * group);
+    int run_exp = -100;  // values: exponent of the largest scale so far
+    const int top_exp = value_top(a.qtype);
+    for (int j = 0; j < T; ++j) {
+      const int s = j % kStages;
+      // the next tile's loads are on their way while this one is decoded
+      load_scales(row1, scn);
+      load_codes(wn, values ? at1 : row1);
+      const int64_t row2 = row_of(j + 2, u);
+      at1 = row_of(j + 2, 8 * group);
+
+      const int tok = sp.base + (tile0 + j) * TK + u;
+      const bool here = row >= 0;
+      // scales of tokens that no row sees count as zero
+      const bool seen = here && tok >= sp.lo && tok < sp.end;
+      float f[NB];
+      uint32_t top = 0;
+      bool bad = false;
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        const uint32_t bits = seen ? sc[x] : 0u;
+        f[x] = half_to_f32<F>(bits);
+        const bool finite = bits < (F == BNB4_BF16 ? 0x7f80u : 0x7c00u);
+        bad = bad || !finite;
+        top = max(top, finite ? bits : 0u);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) ctl->top[values][warp & 3] = top;
+      group_sync(values ? 2 : 1);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) top = max(top, ctl->top[values][x]);
+      int e = F == BNB4_BF16 ? static_cast<int>(top >> 7) - 127 : static_cast<int>(top >> 10) - 15;
+      e = e < -100 ? -100 : e;
+      if (values) e = run_exp = e > run_exp ? e : run_exp;
+      const float norm = pow2(values ? top_exp - e : -e);
+      // fp16 factors; a key row with a scale that is not finite becomes NaN, a
+      // value row zero (the rows that see it are made NaN by the softmax)
+      uint32_t fac[NB];
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        const float y = bad ? (values ? 0.0f : __int_as_float(0x7fffffff)) : f[x] * norm;
+        fac[x] = pack_f16x2(y, y);
+      }
+      Meta& mt = ctl->meta[j % kRing];
+      const unsigned have = __ballot_sync(0xffffffffu, here);
+      const unsigned bads = __ballot_sync(0xffffffffu, bad);
+      if (values) {
+#pragma unroll
+        for (int x = 0; x < NB; ++x) value_scale[x][u] = static_cast<uint16_t>(fac[x]);
+      }
+      if (lane == 0) {
+        if (values) {
+          mt.bad[warp & 3] = bads;
+          if ((warp & 3) == 0) mt.value_exp = e;
+        } else {
+          mt.present[warp & 3] = static_cast<uint8_t>((have & 1u) | ((have >> 15) & 2u));
+          if ((warp & 3) == 0) mt.key_exp = e;
+        }
+        mbar_arrive(bar(ctl->m_full[j % kRing]));
+      }
+      // the products that read this stage last have completed; all of the
+      // group's scales are there
+      if (!group_all(values ? 2 : 1, warp_wait(values ? ctl->v_empty[s] : ctl->k_empty[s],
+                                               ((j / kStages) & 1) ^ 1)))
+        break;
+      if (!values) {
+        uint8_t* dst = smem + S::kOffK + s * S::kK + u * 128;
+#pragma unroll
+        for (int x = 0; x < kWords; ++x) {
+          const uint4 y = dq8(lut, w[x]);
+          // word x holds stored places 8 x ..: of one block, or two of 4 values
+          const int b0 = ((8 * x) % (D / 8)) / (BS / 8);
+          const int b1 = ((8 * x + 4) % (D / 8)) / (BS / 8);
+          *reinterpret_cast<uint4*>(dst + (x / 8) * kHalf + (((x & 7) ^ (u & 7)) << 4)) =
+              make_uint4(mul_f16x2(y.x, fac[b0]), mul_f16x2(y.y, fac[b0]),
+                         mul_f16x2(y.z, fac[b1]), mul_f16x2(y.w, fac[b1]));
+        }
+      } else {
+        // the 8 tokens are piece group % 8 of half group / 8 of the operand's rows
+        uint8_t* half = smem + S::kOffV + s * S::kV + (group / 8) * (D * 128);
+#pragma unroll
+        for (int x = 0; x < kUnits; ++x) {
+          const int word = word0 + x;
+          uint32_t c[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) c[y] = w[8 * x + y];
+          transpose_codes(c);
+          const int b0 = ((8 * word) % (D / 8)) / (BS / 8);
+          const int b1 = ((8 * word + 4) % (D / 8)) / (BS / 8);
+          const uint4 g0 = *reinterpret_cast<const uint4*>(&value_scale[b0][8 * group]);
+          const uint4 g1 = *reinterpret_cast<const uint4*>(&value_scale[b1][8 * group]);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {  // row 8 word + y
+            const uint4 v = dq8(lut, c[y]);
+            const uint4 g = y < 4 ? g0 : g1;
+            *reinterpret_cast<uint4*>(half + (8 * word + y) * 128 + (((group & 7) ^ y) << 4)) =
+                make_uint4(mul_f16x2(v.x, g.x), mul_f16x2(v.y, g.y), mul_f16x2(v.z, g.z),
+                           mul_f16x2(v.w, g.w));
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(values ? ctl->v_full[s] : ctl->k_full[s]));
+      row = row1;
+      row1 = row2;
+#pragma unroll
+      for (int x = 0; x < NB; ++x) sc[x] = scn[x];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) w[x] = wn[x];
+    }
+  } else if (lane == 0) {
+    // -------------------------------------------------------- MMA issuer
+    constexpr uint32_t kBase = (1u << 4) | (static_cast<uint32_t>(TR >> 4) << 24);
+    constexpr uint32_t kIdescS = kBase | (static_cast<uint32_t>(TK >> 3) << 17);
+    constexpr uint32_t kIdescO = kBase | (static_cast<uint32_t>(D >> 3) << 17);
+    const uint32_t q_at = smem_u32(smem), k_at = q_at + S::kOffK, v_at = q_at + S::kOffV;
+    auto product_o = [&](int r, int j) {  // sums += weights of tile j * values
+      if (!wait_bounded(bar(ctl->p_full[r]), j & 1, ctl, a.err) ||
+          !wait_bounded(bar(ctl->v_full[j % kStages]), (j / kStages) & 1, ctl, a.err))
+        return false;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t v = v_at + (j % kStages) * S::kV;
+#pragma unroll
+      for (int k = 0; k < TK / 16; ++k)
+        umma_ts(o_col(r), s_col(r) + 8 * k, sw128_desc(v + (k / 4) * (D * 128) + 32 * (k & 3)),
+                kIdescO, j > 0 || k > 0);
+      return true;
+    };
+    bool ok = T == 0 || wait_bounded(bar(ctl->q_full), 0, ctl, a.err);
+    for (int j = 0; j < T && ok; ++j) {
+      ok = wait_bounded(bar(ctl->k_full[j % kStages]), (j / kStages) & 1, ctl, a.err);
+      for (int r = 0; r < nr && ok; ++r) {
+        if (j > 0) ok = product_o(r, j - 1);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t k = k_at + (j % kStages) * S::kK, q = q_at + r * S::kQ;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          umma_ss(s_col(r), sw128_desc(q + (x / 4) * kHalf + 32 * (x & 3)),
+                  sw128_desc(k + (x / 4) * kHalf + 32 * (x & 3)), kIdescS, x > 0);
+        umma_commit(bar(ctl->s_full[r]));
+      }
+      if (ok) {
+        umma_commit(bar(ctl->k_empty[j % kStages]));
+        if (j > 0) umma_commit(bar(ctl->v_empty[(j - 1) % kStages]));
+      }
+    }
+    for (int r = 0; r < nr && ok && T > 0; ++r) {
+      ok = product_o(r, T - 1);
+      if (ok) umma_commit(bar(ctl->o_full[r]));
+    }
+    if (!ok) {  // products in flight finish before tensor memory is given back
+      umma_commit(bar(ctl->o_full[0]));
+      wait_drain(bar(ctl->o_full[0]), 0, ctl);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+// Joins the splits of an item: one thread per 4 values of a row.
+template <int D, int BS, int F>
+__global__ void __launch_bounds__(256) attn_prefill_join_kernel(const PrefillArgs pa) {
+  const AttnArgs& a = pa.a;
+  pdl_wait();
+  const int pairs = a.batch * a.heads;
+  constexpr int kPerItem = kRowsCta * (D / 4) / 256;  // CTAs per item
+  const int item = static_cast<int>(blockIdx.x) / kPerItem;
+  const int pair = item % pairs, rt = a.row_tiles - 1 - item / pairs;
+  const int h = pair % a.heads, b = pair / a.heads;
+  const Span sp = span_of<kRowsCta, TK>(a, b, rt);
+  const int e = (static_cast<int>(blockIdx.x) - item * kPerItem) * 256 + threadIdx.x;
+  const int row = e / (D / 4), x = (e % (D / 4)) * 4;
+  if (row >= sp.rows) return;
+  constexpr int64_t kPart = kRowsCta * (D + 2);
+  const float* part = a.ws + static_cast<int64_t>(item) * pa.splits * kPart;
+  float top = -INFINITY;
+  for (int s = 0; s < pa.splits; ++s) top = fmaxf(top, part[s * kPart + kRowsCta * D + 2 * row]);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < pa.splits; ++s) {
+    const float2 ml =
+        *reinterpret_cast<const float2*>(part + s * kPart + kRowsCta * D + 2 * row);
+    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // saw nothing; its sums may be unwritten
+    const float f = ex2(ml.x - ref);
+    const float4 y = *reinterpret_cast<const float4*>(part + s * kPart + row * D + x);
+    // a NaN sum of a part without a maximum stays NaN
+    sum += ml.x == -INFINITY ? ml.y : ml.y * f;
+    v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y);
+    v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+  }
+  const RowOut<F> out(a, sp, h, sp.r0 + row, top, sum, x == 0);
+  const int d = value_at<D, BS>(x);
+  out.pair(d, v.x, v.y);
+  out.pair(d + 2, v.z, v.w);
+}
+
+// ------------------------------------------------------------------- host
+// Splits of the tokens where the row tiles alone leave SMs idle: as many as
+// fill the SMs once, each at least 4 tiles long.
+int splits_for(int64_t items, int64_t span, int num_sms) {
+  const int64_t tiles = (span + TK - 1) / TK;
+  int64_t s = items > 0 ? num_sms / items : 1;
+  if (s > tiles / 4) s = tiles / 4;
+  return s < 2 ? 1 : static_cast<int>(s);
+}
+
+template <int D, int BS, int F>
+cudaError_t launch_t(const PrefillArgs& pa, int64_t items, cudaStream_t s) {
+  constexpr int kSmem = Smem<D>::kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
+  static_assert(kSmem + 2048 <= 232448, "shared memory budget");
+  auto kern = attn_prefill_kernel<D, BS, F>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(kern, dim3(static_cast<unsigned>(items * pa.splits)), dim3(kThreads), kSmem, s,
+                    programmatic_after_kernel(s), pa);
+  if (e != cudaSuccess || pa.splits == 1) return e;
+  return launch_kernel(attn_prefill_join_kernel<D, BS, F>,
+                       dim3(static_cast<unsigned>(items * (kRowsCta * (D / 4) / 256))), dim3(256),
+                       0, s, true, pa);
+}
+
+int64_t items_of(const AttnArgs& a, int64_t rows) {
+  return static_cast<int64_t>(a.batch) * a.heads * ((rows + kRowsCta - 1) / kRowsCta);
+}
+
+}  // namespace
+
+size_t attn_prefill_workspace(const AttnArgs& a, int head_dim, int64_t rows, int64_t span,
+                              int num_sms) {
+  const int64_t items = items_of(a, rows);
+  const int splits = splits_for(items, span, num_sms);
+  return splits == 1 ? 0
+                     : sizeof(float) * static_cast<size_t>(items) * splits * kRowsCta *
+                           (static_cast<size_t>(head_dim) + 2);
+}
+
+cudaError_t launch_attn_prefill(AttnArgs& a, const bnb4_kv_cache& c, int64_t rows, int64_t span,
+                                int num_sms, cudaStream_t s) {
+  PrefillArgs pa;
+  a.row_tiles = static_cast<int>((rows + kRowsCta - 1) / kRowsCta);
+  const int64_t items = items_of(a, rows);
+  pa.splits = splits_for(items, span, num_sms);
+  pa.a = a;
+#define BNB4_PREFILL(DV, BSV)                                       \
+  return c.dtype == BNB4_F16 ? launch_t<DV, BSV, BNB4_F16>(pa, items, s)  \
+                             : launch_t<DV, BSV, BNB4_BF16>(pa, items, s);
+  if (c.head_dim == 128) {
+    if (c.blocksize == 128) { BNB4_PREFILL(128, 128) }
+    if (c.blocksize == 64) { BNB4_PREFILL(128, 64) }
+    BNB4_PREFILL(128, 32)
+  }
+  if (c.blocksize == 64) { BNB4_PREFILL(64, 64) }
+  BNB4_PREFILL(64, 32)
+#undef BNB4_PREFILL
+}
+
+}  // namespace bnb4

@@ -491,7 +491,7 @@ typedef struct bnb4_attn {
   int32_t n_heads;
   int32_t max_q_len;
   int32_t max_seq_len;
-  int32_t block_table_width;
+  int32_t block_table_width; /* times page_size at most 2^30 */
   int32_t causal;  /* 0 or 1 */
   int32_t window;  /* 0: none */
   float scale;     /* 1e-8 .. 1e8 */
