@@ -7,24 +7,24 @@
 // 128 tokens; what bounds it is the instruction issue and the exponentials of
 // the softmax, next to which the cache's decode has to fit.
 //
-// Roles of a CTA's 17 warps (one CTA per SM):
+// Roles of a CTA's 16 warps (one CTA per SM):
 //  * warps 0-3 and 4-7: the softmax of row tile 0 and 1, one row per thread.
 //    Scores are read from tensor memory twice (their maximum; then the
 //    weights), 32 at a time, so a row never needs 128 registers.  The running
 //    maximum is only raised when it grows by more than 8 binades; until then
 //    weights exceed one, and the sums in tensor memory need no rescaling.
 //    The weights go back to tensor memory, over the scores, as the A operand
-//    of the second product.
+//    of the second product.  One thread of each row tile then issues its
+//    products: the sums of this tile of tokens and the scores of the next; the
+//    row tiles run apart, so one's products run under the other's softmax.
 //  * warps 8-11: the keys.  Thread r owns token r of the tile: 64 codes a
-//    64-byte row in registers one tile ahead, looked up by byte permutes in
-//    the constant table, times the block's scale, into the swizzled K-major
-//    operand.
-//  * warps 12-15: the values.  Thread u owns 8 tokens x 8 values: its 8 words
-//    of codes are transposed nibble by nibble in registers (3 butterfly
-//    steps), so that the operand (values as rows, tokens as K) is again
-//    written 8 codes and 16 bytes at a time.
-//  * warp 16: tensor memory and the issue of both products; the two row tiles
-//    take turns, so one's products run under the other's softmax.
+//    64-byte row in registers one tile ahead, looked up two at a time (a byte)
+//    in a table of fp16 pairs in shared memory, times the block's scale, into
+//    the swizzled K-major operand.
+//  * warps 12-15: the values.  Thread u owns 8 tokens x 8 or 16 values; bytes
+//    of two tokens' codes of the same value are put together first, so that
+//    the operand (values as rows, tokens as K) is again written 8 codes and 16
+//    bytes at a time.
 // The stored order of a row's values is kept for K and q alike (a dot product
 // does not care) and undone when the output is written.
 //
@@ -37,7 +37,6 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "kvcache.h"
-#include "lut.cuh"
 #include "sm100.cuh"
 
 namespace bnb4 {
@@ -46,8 +45,8 @@ namespace {
 constexpr int TK = 128;        // tokens per tile
 constexpr int TR = 128;        // rows per row tile (threads of a softmax group)
 constexpr int kRowsCta = 2 * TR;
-constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16;
-constexpr int kThreads = 17 * 32;
+constexpr int kKeyWarp = 8, kValueWarp = 12;
+constexpr int kThreads = 16 * 32;
 constexpr int kStages = 2;     // decoded tiles of keys, and of values
 constexpr int kRing = 4;       // tiles' scalars: see Meta
 constexpr float kLazy = 8.0f;  // growth of the maximum that is let pass, in binades
@@ -64,13 +63,14 @@ struct Smem {
   static constexpr int kV = (TK / 64) * D * 128;     // one tile of values
   static constexpr int kOffK = 2 * kQ;
   static constexpr int kOffV = kOffK + kStages * kK;
-  static constexpr int kOffCtl = kOffV + kStages * kV;
+  static constexpr int kOffTable = kOffV + kStages * kV;
+  static constexpr int kOffCtl = kOffTable + 256 * 128;
 };
 
 // A tile's scalars, in a ring of 4: tile j + 4's are written after the scores
-// of tile j + 2 were asked for, hence after both row tiles' softmax of tile j
-// + 1 -- the last readers of tile j's are done, and a wait never falls two
-// phases behind.
+// of tile j + 1 were complete for both row tiles (k_empty), hence after their
+// softmax of tile j -- its readers are done, and a wait never falls two phases
+// behind.
 struct Meta {
   int key_exp, value_exp;   // keys are held times 2^-key_exp, values 2^(top - value_exp)
   uint8_t present[4];       // per key warp: bit s: its sub-tile s (16 tokens) is cached
@@ -78,7 +78,7 @@ struct Meta {
 };
 
 struct Ctl {
-  uint64_t q_full, s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], o_full[2];  // a row tile's scores, and its sums, are complete
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t m_full[kRing];
   uint64_t wait_limit_ns;
@@ -172,51 +172,29 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
   return r != 0;
 }
 
-// The table times its constant, in fp16, as two byte-split halves.
-__device__ __forceinline__ Lut make_table(int qtype) {
-  uint32_t P[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float n0 = __fmul_rn(nf4_value(2 * j), kNf4Scale);
-    const float n1 = __fmul_rn(nf4_value(2 * j + 1), kNf4Scale);
-    // E2M1's magnitudes, exact
-    constexpr float e[8] = {0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f};
-    const float sgn = j >= 4 ? -1.0f : 1.0f;
-    P[j] = qtype == kQtNF4 ? pack_f16x2(n0, n1)
-                           : pack_f16x2(sgn * e[(2 * j) & 7], sgn * e[(2 * j + 1) & 7]);
+// The table of code pairs: entry `byte` holds the fp16 pair {t[byte >> 4],
+// t[byte & 15]} (times the table's constant), one copy per bank.
+__device__ __forceinline__ void build_pairs(uint32_t at, int qtype, int warp, int warps) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  const float v = qtype == kQtNF4 ? __fmul_rn(nf4_value(c), kNf4Scale)
+                                  : rintf(__fmul_rn(code_value(kQtFP4, c), 12.0f)) * 0.5f;
+  const uint32_t h = pack_f16x2(v, 0.0f) & 0xffffu;
+  for (int e = warp; e < 256; e += warps) {
+    const uint32_t x = __shfl_sync(0xffffffffu, h, e >> 4) | __shfl_sync(0xffffffffu, h, e & 15) << 16;
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128u * e + 4u * lane), "r"(x) : "memory");
   }
-  Lut l;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    l.L[q] = prmt(P[2 * q], P[2 * q + 1], 0x6420);
-    l.H[q] = prmt(P[2 * q], P[2 * q + 1], 0x7531);
-  }
-  return l;
 }
-
-// 8 words of 8 codes (byte j = codes 2 j, 2 j + 1, the first in the high
-// nibble): word i's code k becomes word k's code i.
-__device__ __forceinline__ void transpose_codes(uint32_t (&w)[8]) {
-  // exchange halves at distance 4 words / 16 bits, 2 / 8, then nibbles
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = w[i], b = w[i + 4];
-    w[i] = prmt(a, b, 0x5410);
-    w[i + 4] = prmt(a, b, 0x7632);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if ((i & 2) == 0) {
-      const uint32_t a = w[i], b = w[i + 2];
-      w[i] = prmt(a, b, 0x6240);
-      w[i + 2] = prmt(a, b, 0x7351);
-    }
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const uint32_t a = w[i], b = w[i + 1];
-    w[i] = (a & 0xf0f0f0f0u) | ((b >> 4) & 0x0f0f0f0fu);
-    w[i + 1] = ((a << 4) & 0xf0f0f0f0u) | (b & 0x0f0f0f0fu);
-  }
+// The pair of byte I of w; lane_table: the table's shared address + 4 * lane.
+template <int I>
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_table) {
+  uint32_t at, v;
+  asm("{\n\t.reg .b32 b;\n\t"
+      "prmt.b32 b, %1, 0, %3;\n\t"
+      "mad.lo.u32 %0, b, 128, %2;\n\t}"
+      : "=r"(at)
+      : "r"(w), "r"(lane_table), "n"(0x4440 | I));
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
 }
 
 // Stored place x (a multiple of 4) of a row -> the value's number in the row.
@@ -244,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
   __shared__ __align__(16) uint16_t value_scale[NB][TK];  // fp16, of the tile being decoded
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
+  build_pairs(smem_u32(smem + S::kOffTable), a.qtype, warp, kThreads / 32);
   pdl_wait();
 
   // this CTA's rows (the tiles with the most tokens first) and tokens
@@ -264,24 +243,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
   auto bar = [&](uint64_t& x) { return smem_u32(&x); };
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(ctl->q_full), 4 * nr);
     for (int r = 0; r < 2; ++r) {
       mbar_init(bar(ctl->s_full[r]), 1);
-      mbar_init(bar(ctl->p_full[r]), 4);
       mbar_init(bar(ctl->o_full[r]), 1);
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(ctl->k_full[s]), 4);
-      mbar_init(bar(ctl->k_empty[s]), 1);
+      mbar_init(bar(ctl->k_empty[s]), nr);
       mbar_init(bar(ctl->v_full[s]), 4);
-      mbar_init(bar(ctl->v_empty[s]), 1);
+      mbar_init(bar(ctl->v_empty[s]), nr);
     }
     for (int s = 0; s < kRing; ++s) mbar_init(bar(ctl->m_full[s]), 8);
     ctl->abort = 0;
     ctl->wait_limit_ns = kWaitLimitNs;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) {
+  if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&ctl->tmem_base)),
                  "r"(512));
@@ -303,6 +280,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
 
   if (warp < kKeyWarp) {
     // ------------------------------------------------------------ softmax
+    constexpr uint32_t kBase = (1u << 4) | (static_cast<uint32_t>(TR >> 4) << 24);
+    constexpr uint32_t kIdescS = kBase | (static_cast<uint32_t>(TK >> 3) << 17);
+    constexpr uint32_t kIdescO = kBase | (static_cast<uint32_t>(D >> 3) << 17);
+    const uint32_t q_at = smem_u32(smem), k_at = q_at + S::kOffK, v_at = q_at + S::kOffV;
+    // the issuing thread's two products; false when a wait gave up
+    auto product_s = [&](int r, int j) {  // scores = q * keys of tile j
+      if (!wait_bounded(bar(ctl->k_full[j % kStages]), (j / kStages) & 1, ctl, a.err)) return false;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t k = k_at + (j % kStages) * S::kK, q = q_at + r * S::kQ;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+        umma_ss(s_col(r), sw128_desc(q + (x / 4) * kHalf + 32 * (x & 3)),
+                sw128_desc(k + (x / 4) * kHalf + 32 * (x & 3)), kIdescS, x > 0);
+      umma_commit(bar(ctl->s_full[r]));
+      umma_commit(bar(ctl->k_empty[j % kStages]));
+      return true;
+    };
+    auto product_o = [&](int r, int j) {  // sums += weights of tile j * values
+      if (!wait_bounded(bar(ctl->v_full[j % kStages]), (j / kStages) & 1, ctl, a.err)) return false;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t v = v_at + (j % kStages) * S::kV;
+#pragma unroll
+      for (int k = 0; k < TK / 16; ++k)
+        umma_ts(o_col(r), s_col(r) + 8 * k, sw128_desc(v + (k / 4) * (D * 128) + 32 * (k & 3)),
+                kIdescO, j > 0 || k > 0);
+      umma_commit(bar(ctl->v_empty[j % kStages]));
+      return true;
+    };
     const int r = warp >> 2;
     if (r < nr) {
       const int row = static_cast<int>(threadIdx.x);  // of the CTA's 256
@@ -355,9 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           *reinterpret_cast<uint4*>(dst + (c / 8) * kHalf + (((c & 7) ^ (row & 7)) << 4)) = y;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(ctl->q_full));
+        group_sync(3 + r);  // all of the row tile's q is there
       }
+      const bool issuer = (threadIdx.x & (TR - 1)) == 0;
+      if (issuer && T > 0) product_s(r, 0);  // a wait that gives up ends the others, too
       // what this row sees, and what all rows of the row tile see
       const int pos = sp.first + rr / a.group;
       const int see_hi = !real ? -1 : a.causal && pos < sp.len ? pos : sp.len - 1;
@@ -371,7 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
       int ve = 0;
       bool ok = true;
       for (int j = 0; j < T; ++j) {
-        if (!warp_wait(ctl->s_full[r], j & 1) || !warp_wait(ctl->m_full[j % kRing], (j / kRing) & 1)) {
+        // (the group's warps meet below: they leave together)
+        if (!group_all(3 + r, warp_wait(ctl->s_full[r], j & 1) &&
+                                  warp_wait(ctl->m_full[j % kRing], (j / kRing) & 1))) {
           ok = false;
           break;
         }
@@ -387,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         const int lo = see_lo - j0, hi = see_hi - j0;
         float v[32];
         float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < TK / 32; ++c) {
           tmem_load32(s_col(r) + lanes + 32 * c, v);
           if (masked) {
@@ -424,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         ve = tve;
         const float ref = (m == -INFINITY ? 0.0f : m) - static_cast<float>(kBoost);
         float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < TK / 32; ++c) {
           tmem_load32(s_col(r) + lanes + 32 * c, v);
           uint32_t p[16];
@@ -452,10 +460,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
               if (x >= lo && x <= hi) l = __int_as_float(0x7fffffff);
         tmem_store_done();
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        group_sync(3 + r);  // all of the row tile's weights are there
+        if (issuer) {
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (product_o(r, j)) {
+            if (j + 1 < T)
+              product_s(r, j + 1);
+            else
+              umma_commit(bar(ctl->o_full[r]));
+          }
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(ctl->p_full[r]));
       }
       // ---------------------------------------------------------- output
+      if (!ok && issuer) {  // products in flight finish before tensor memory is given back
+        umma_commit(bar(ctl->o_full[r]));
+        wait_drain(bar(ctl->o_full[r]), 0, ctl);
+      }
       if (ok && T > 0) {
         ok = warp_wait(ctl->o_full[r], 0);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -518,24 +539,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         }
       }
     }
-  } else if (warp < kMmaWarp) {
+  } else {
     // ------------------------------------------- keys and values: decode
     const bool values = warp >= kValueWarp;
     const int u = static_cast<int>(threadIdx.x) - (values ? kValueWarp : kKeyWarp) * 32;
-    const Lut lut = make_table(a.qtype);
-    // token u of the tile: its cache row, or -1
-    auto row_of = [&](int tile, int tok) {
-      int64_t row = -1;
+    const uint32_t lane_table = smem_u32(smem + S::kOffTable) + 4u * lane;
+    // a token's page entry, read two tiles ahead (-1: not cached), and its cache
+    // row, computed when the entry has arrived
+    auto entry_of = [&](int tile, int tok) {
       const int j = sp.base + (tile0 + tile) * TK + tok;
       // whole sub-tiles of 16 tokens are brought in (a page holds them whole)
-      if (tile < T && (j & ~15) < sp.end) {
-        const uint32_t x = a.page.div(static_cast<uint32_t>(j));
-        const int p = __ldg(bt + x);
-        if (p >= 0 && p < a.num_pages)
-          row = (static_cast<int64_t>(p) * a.heads + h) * a.page.d +
-                (static_cast<uint32_t>(j) - x * a.page.d);
-      }
-      return row;
+      return tile < T && (j & ~15) < sp.end ? __ldg(bt + a.page.div(static_cast<uint32_t>(j))) : -1;
+    };
+    auto row_of = [&](int entry, int tile, int tok) {
+      const uint32_t j = static_cast<uint32_t>(sp.base + (tile0 + tile) * TK + tok);
+      const uint32_t in = j - a.page.div(j) * a.page.d;
+      return entry >= 0 && entry < a.num_pages
+                 ? (static_cast<int64_t>(entry) * a.heads + h) * a.page.d + in
+                 : static_cast<int64_t>(-1);
     };
     // scales of token u: raw patterns
     const uint16_t* absmax = values ? a.v_absmax : a.k_absmax;
@@ -550,10 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
     const int group = (lane & 7) + 8 * (warp & 1);
     const int word0 = kUnits * ((lane >> 3) + 4 * ((warp >> 1) & 1));
     uint32_t w[16], wn[16];
-    // rows of this tile's token, and of the next tile's: a key thread's token,
-    // a value thread's first of 8
-    int64_t row = row_of(0, u);
-    int64_t row1 = row_of(1, u), at1 = row_of(0, 8 * group);
+    const int first = values ? 8 * group : u;  // the thread's codes start at this token
     auto load_codes = [&](uint32_t (&x)[16], int64_t at) {
       if (!values) {
 #pragma unroll
@@ -577,18 +595,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
       }
     };
     uint32_t sc[NB], scn[NB];
+    int64_t row = row_of(entry_of(0, u), 0, u);  // cache row of token u of this tile
     load_scales(row, sc);
-    load_codes(w, values ? at1 : row);
-    at1 = row_of(1, 8 * group);
+    load_codes(w, row_of(entry_of(0, first), 0, first));
+    int e1 = entry_of(1, u), c1 = entry_of(1, first);  // the next tile's entries
     int run_exp = -100;  // values: exponent of the largest scale so far
     const int top_exp = value_top(a.qtype);
     for (int j = 0; j < T; ++j) {
       const int s = j % kStages;
       // the next tile's loads are on their way while this one is decoded
+      const int64_t row1 = row_of(e1, j + 1, u);
       load_scales(row1, scn);
-      load_codes(wn, values ? at1 : row1);
-      const int64_t row2 = row_of(j + 2, u);
-      at1 = row_of(j + 2, 8 * group);
+      load_codes(wn, row_of(c1, j + 1, first));
+      e1 = entry_of(j + 2, u);
+      c1 = entry_of(j + 2, first);
 
       const int tok = sp.base + (tile0 + j) * TK + u;
       const bool here = row >= 0;
@@ -648,7 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         uint8_t* dst = smem + S::kOffK + s * S::kK + u * 128;
 #pragma unroll
         for (int x = 0; x < kWords; ++x) {
-          const uint4 y = dq8(lut, w[x]);
+          const uint4 y = make_uint4(pair_of<0>(w[x], lane_table), pair_of<1>(w[x], lane_table),
+                                     pair_of<2>(w[x], lane_table), pair_of<3>(w[x], lane_table));
           // word x holds stored places 8 x ..: of one block, or two of 4 values
           const int b0 = ((8 * x) % (D / 8)) / (BS / 8);
           const int b1 = ((8 * x + 4) % (D / 8)) / (BS / 8);
@@ -662,83 +683,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
 #pragma unroll
         for (int x = 0; x < kUnits; ++x) {
           const int word = word0 + x;
-          uint32_t c[8];
+          // bytes of two tokens' codes: of the word's even values, and its odd ones
+          uint32_t ev[4], od[4];
 #pragma unroll
-          for (int y = 0; y < 8; ++y) c[y] = w[8 * x + y];
-          transpose_codes(c);
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t t0 = w[8 * x + 2 * y], t1 = w[8 * x + 2 * y + 1];
+            ev[y] = (t0 & 0xf0f0f0f0u) | ((t1 >> 4) & 0x0f0f0f0fu);
+            od[y] = ((t0 << 4) & 0xf0f0f0f0u) | (t1 & 0x0f0f0f0fu);
+          }
           const int b0 = ((8 * word) % (D / 8)) / (BS / 8);
           const int b1 = ((8 * word + 4) % (D / 8)) / (BS / 8);
           const uint4 g0 = *reinterpret_cast<const uint4*>(&value_scale[b0][8 * group]);
-          const uint4 g1 = *reinterpret_cast<const uint4*>(&value_scale[b1][8 * group]);
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {  // row 8 word + y
-            const uint4 v = dq8(lut, c[y]);
+          const uint4 g1 =
+              BS == 32 ? *reinterpret_cast<const uint4*>(&value_scale[b1][8 * group]) : g0;
+          auto row_out = [&](int y, uint32_t p0, uint32_t p1, uint32_t p2, uint32_t p3) {
             const uint4 g = y < 4 ? g0 : g1;
             *reinterpret_cast<uint4*>(half + (8 * word + y) * 128 + (((group & 7) ^ y) << 4)) =
-                make_uint4(mul_f16x2(v.x, g.x), mul_f16x2(v.y, g.y), mul_f16x2(v.z, g.z),
-                           mul_f16x2(v.w, g.w));
-          }
+                make_uint4(mul_f16x2(p0, g.x), mul_f16x2(p1, g.y), mul_f16x2(p2, g.z),
+                           mul_f16x2(p3, g.w));
+          };
+#define BNB4_VALUE_ROWS(I)                                                                   \
+  row_out(2 * I, pair_of<I>(ev[0], lane_table), pair_of<I>(ev[1], lane_table),               \
+          pair_of<I>(ev[2], lane_table), pair_of<I>(ev[3], lane_table));                     \
+  row_out(2 * I + 1, pair_of<I>(od[0], lane_table), pair_of<I>(od[1], lane_table),           \
+          pair_of<I>(od[2], lane_table), pair_of<I>(od[3], lane_table));
+          BNB4_VALUE_ROWS(0)
+          BNB4_VALUE_ROWS(1)
+          BNB4_VALUE_ROWS(2)
+          BNB4_VALUE_ROWS(3)
+#undef BNB4_VALUE_ROWS
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(values ? ctl->v_full[s] : ctl->k_full[s]));
       row = row1;
-      row1 = row2;
 #pragma unroll
       for (int x = 0; x < NB; ++x) sc[x] = scn[x];
 #pragma unroll
       for (int x = 0; x < 16; ++x) w[x] = wn[x];
     }
-  } else if (lane == 0) {
-    // -------------------------------------------------------- MMA issuer
-    constexpr uint32_t kBase = (1u << 4) | (static_cast<uint32_t>(TR >> 4) << 24);
-    constexpr uint32_t kIdescS = kBase | (static_cast<uint32_t>(TK >> 3) << 17);
-    constexpr uint32_t kIdescO = kBase | (static_cast<uint32_t>(D >> 3) << 17);
-    const uint32_t q_at = smem_u32(smem), k_at = q_at + S::kOffK, v_at = q_at + S::kOffV;
-    auto product_o = [&](int r, int j) {  // sums += weights of tile j * values
-      if (!wait_bounded(bar(ctl->p_full[r]), j & 1, ctl, a.err) ||
-          !wait_bounded(bar(ctl->v_full[j % kStages]), (j / kStages) & 1, ctl, a.err))
-        return false;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t v = v_at + (j % kStages) * S::kV;
-#pragma unroll
-      for (int k = 0; k < TK / 16; ++k)
-        umma_ts(o_col(r), s_col(r) + 8 * k, sw128_desc(v + (k / 4) * (D * 128) + 32 * (k & 3)),
-                kIdescO, j > 0 || k > 0);
-      return true;
-    };
-    bool ok = T == 0 || wait_bounded(bar(ctl->q_full), 0, ctl, a.err);
-    for (int j = 0; j < T && ok; ++j) {
-      ok = wait_bounded(bar(ctl->k_full[j % kStages]), (j / kStages) & 1, ctl, a.err);
-      for (int r = 0; r < nr && ok; ++r) {
-        if (j > 0) ok = product_o(r, j - 1);
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t k = k_at + (j % kStages) * S::kK, q = q_at + r * S::kQ;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          umma_ss(s_col(r), sw128_desc(q + (x / 4) * kHalf + 32 * (x & 3)),
-                  sw128_desc(k + (x / 4) * kHalf + 32 * (x & 3)), kIdescS, x > 0);
-        umma_commit(bar(ctl->s_full[r]));
-      }
-      if (ok) {
-        umma_commit(bar(ctl->k_empty[j % kStages]));
-        if (j > 0) umma_commit(bar(ctl->v_empty[(j - 1) % kStages]));
-      }
-    }
-    for (int r = 0; r < nr && ok && T > 0; ++r) {
-      ok = product_o(r, T - 1);
-      if (ok) umma_commit(bar(ctl->o_full[r]));
-    }
-    if (!ok) {  // products in flight finish before tensor memory is given back
-      umma_commit(bar(ctl->o_full[0]));
-      wait_drain(bar(ctl->o_full[0]), 0, ctl);
-    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == 0) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
@@ -795,7 +783,7 @@ int splits_for(int64_t items, int64_t span, int num_sms) {
 template <int D, int BS, int F>
 cudaError_t launch_t(const PrefillArgs& pa, int64_t items, cudaStream_t s) {
   constexpr int kSmem = Smem<D>::kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
-  static_assert(kSmem + 2048 <= 232448, "shared memory budget");
+  static_assert(kSmem + (D / BS) * TK * 2 <= 232448, "shared memory budget");
   auto kern = attn_prefill_kernel<D, BS, F>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
