@@ -7,16 +7,15 @@
 // 128 tokens; what bounds it is the instruction issue and the exponentials of
 // the softmax, next to which the cache's decode has to fit.
 //
-// Roles of a CTA's 16 warps (one CTA per SM):
+// Roles of a CTA's 18 warps (one CTA per SM):
 //  * warps 0-3 and 4-7: the softmax of row tile 0 and 1, one row per thread.
-//    Scores are read from tensor memory twice (their maximum; then the
-//    weights), 32 at a time, so a row never needs 128 registers.  The running
+//    Tokens are taken 64 at a time, in two halves of the scores' columns: a
+//    half's next scores are computed while the other half's weights form, so
+//    the softmax does not wait for the products.  The running
 //    maximum is only raised when it grows by more than 8 binades; until then
 //    weights exceed one, and the sums in tensor memory need no rescaling.
 //    The weights go back to tensor memory, over the scores, as the A operand
-//    of the second product.  One thread of each row tile then issues its
-//    products: the sums of this tile of tokens and the scores of the next; the
-//    row tiles run apart, so one's products run under the other's softmax.
+//    of the second product.
 //  * warps 8-11: the keys.  Thread r owns token r of the tile: 64 codes a
 //    64-byte row in registers one tile ahead, looked up two at a time (a byte)
 //    in a table of fp16 pairs in shared memory, times the block's scale, into
@@ -25,6 +24,10 @@
 //    of two tokens' codes of the same value are put together first, so that
 //    the operand (values as rows, tokens as K) is again written 8 codes and 16
 //    bytes at a time.
+//  * warps 16 and 17 issue the products of row tile 0 and 1: the sums of a half
+//    and the scores of the next one to take its columns.  (A wait, a commit
+//    and a product each cost the issuing warp around a hundred cycles: done by
+//    a softmax warp, or by one warp for both row tiles, they set the pace.)
 // The stored order of a row's values is kept for K and q alike (a dot product
 // does not care) and undone when the output is written.
 //
@@ -42,11 +45,12 @@
 namespace bnb4 {
 namespace {
 
-constexpr int TK = 128;        // tokens per tile
+constexpr int TK = 128;        // tokens per decoded tile
+constexpr int TH = TK / 2;     // tokens per step of the softmax
 constexpr int TR = 128;        // rows per row tile (threads of a softmax group)
 constexpr int kRowsCta = 2 * TR;
-constexpr int kKeyWarp = 8, kValueWarp = 12;
-constexpr int kThreads = 16 * 32;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kIssueWarp = 16;
+constexpr int kThreads = 18 * 32;
 constexpr int kStages = 2;     // decoded tiles of keys, and of values
 constexpr int kRing = 4;       // tiles' scalars: see Meta
 constexpr float kLazy = 8.0f;  // growth of the maximum that is let pass, in binades
@@ -78,7 +82,9 @@ struct Meta {
 };
 
 struct Ctl {
-  uint64_t s_full[2], o_full[2];  // a row tile's scores, and its sums, are complete
+  // of a row tile: q is there; a half's scores and its weights are complete;
+  // the sums are, but for the last half, and in the end
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2], done[2];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t m_full[kRing];
   uint64_t wait_limit_ns;
@@ -88,26 +94,41 @@ struct Ctl {
   Meta meta[kRing];
 };
 
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
+// The products are issued by a whole warp, of which one lane (`one` != 0) acts:
+// so descriptors and addresses stay in uniform registers.  A descriptor is
+// given by its low word (the address / 16); the high word is a constant.
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo) {
+  return static_cast<uint64_t>(static_cast<uint32_t>(sw128_desc(0) >> 32)) << 32 | lo;
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) {
+  return static_cast<uint32_t>(sw128_desc(addr));
+}
+__device__ __forceinline__ void umma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b,
+                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(one),
+      "r"(d), "l"(desc_at(a)), "l"(desc_at(b)), "r"(idesc), "r"(accumulate));
 }
 // the A operand in tensor memory
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b,
+                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(one),
+      "r"(d), "r"(a), "l"(desc_at(b)), "r"(idesc), "r"(accumulate));
 }
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
+__device__ __forceinline__ void umma_commit(uint32_t one, uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(
+          one),
+      "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
@@ -122,19 +143,27 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(at));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t at, const float (&v)[32]) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+// Loads have arrived: the registers may be used (and are tied to this point).
+__device__ __forceinline__ void tmem_load_done(float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
       : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
@@ -158,20 +187,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void group_sync(int id) {
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
-// The same, and whether all of them bring true: they leave their loop together.
-__device__ __forceinline__ bool group_all(int id, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.and.pred p, %2, 128, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(ok ? 1u : 0u), "r"(id)
-      : "memory");
-  return r != 0;
-}
-
 // The table of code pairs: entry `byte` holds the fp16 pair {t[byte >> 4],
 // t[byte & 15]} (times the table's constant), one copy per bank.
 __device__ __forceinline__ void build_pairs(uint32_t at, int qtype, int warp, int warps) {
@@ -197,6 +212,20 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_table) {
   return v;
 }
 
+// Columns outside lo .. hi, and of sub-tiles (a bit per 16) that are not
+// present, are not seen.
+__device__ __forceinline__ uint32_t mask_bits(uint32_t present, int lo, int hi) {
+  uint32_t k = ((present & 1u) ? 0x0000ffffu : 0u) | ((present & 2u) ? 0xffff0000u : 0u);
+  if (lo > 0) k = lo > 31 ? 0u : k & (0xffffffffu << lo);
+  if (hi < 31) k = hi < 0 ? 0u : k & (0xffffffffu >> (31 - hi));
+  return k;
+}
+__device__ __forceinline__ void mask32(float (&v)[32], uint32_t present, int lo, int hi) {
+  const uint32_t k = mask_bits(present, lo, hi);
+#pragma unroll
+  for (int x = 0; x < 32; ++x) v[x] = (k >> x) & 1u ? v[x] : -INFINITY;
+}
+
 // Stored place x (a multiple of 4) of a row -> the value's number in the row.
 template <int D, int BS>
 __device__ __forceinline__ constexpr int value_at(int x) {
@@ -220,7 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + S::kOffCtl);
   __shared__ __align__(16) uint16_t value_scale[NB][TK];  // fp16, of the tile being decoded
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same in every lane, in a form the compiler can see
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
+  const int lane = threadIdx.x & 31;
   pdl_trigger();
   build_pairs(smem_u32(smem + S::kOffTable), a.qtype, warp, kThreads / 32);
   pdl_wait();
@@ -237,15 +268,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
   const int per = (sp.tiles + pa.splits - 1) / pa.splits;
   const int tile0 = split * per < sp.tiles ? split * per : sp.tiles;
   const int tile1 = tile0 + per < sp.tiles ? tile0 + per : sp.tiles;
-  const int T = tile1 - tile0;  // 0: nothing to add (a partial result of no weight)
-  const int nr = sp.rows > TR ? 2 : 1;
+  // 0: nothing to add (a partial result of no weight)
+  const int T = __shfl_sync(0xffffffffu, tile1 - tile0, 0);
+  const int nr = __shfl_sync(0xffffffffu, sp.rows > TR ? 2 : 1, 0);
   const int32_t* bt = a.block_table + static_cast<int64_t>(b) * a.bt_stride;
   auto bar = [&](uint64_t& x) { return smem_u32(&x); };
 
   if (threadIdx.x == 0) {
     for (int r = 0; r < 2; ++r) {
-      mbar_init(bar(ctl->s_full[r]), 1);
+      mbar_init(bar(ctl->s_full[r][0]), 1);
+      mbar_init(bar(ctl->s_full[r][1]), 1);
       mbar_init(bar(ctl->o_full[r]), 1);
+      mbar_init(bar(ctl->done[r]), 1);
+      mbar_init(bar(ctl->q_full[r]), 4);
+      mbar_init(bar(ctl->p_full[r][0]), 4);
+      mbar_init(bar(ctl->p_full[r][1]), 4);
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(ctl->k_full[s]), 4);
@@ -267,47 +304,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   // columns: scores (and weights over them) of row tile r at 128 r, sums at 256 + 128 r
   auto s_col = [&](int r) { return tmem + 128u * r; };
   auto o_col = [&](int r) { return tmem + 256u + 128u * r; };
-  // one decision per warp: lane 0 waits, the others follow
+  // a thread's bounded wait; once one has given up, all return at once
+  auto wait_here = [&](uint64_t& x, uint32_t parity) {
+    if (!mbar_try_wait<false>(bar(x), parity) && *reinterpret_cast<volatile int*>(&ctl->abort) == 0)
+      wait_bounded(bar(x), parity, ctl, a.err);
+  };
   auto warp_wait = [&](uint64_t& x, uint32_t parity) {
-    bool w = true;
-    if (lane == 0) w = wait_bounded(bar(x), parity, ctl, a.err);
-    return __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
+    if (lane == 0) wait_here(x, parity);
+    __syncwarp();
   };
 
   if (warp < kKeyWarp) {
     // ------------------------------------------------------------ softmax
-    constexpr uint32_t kBase = (1u << 4) | (static_cast<uint32_t>(TR >> 4) << 24);
-    constexpr uint32_t kIdescS = kBase | (static_cast<uint32_t>(TK >> 3) << 17);
-    constexpr uint32_t kIdescO = kBase | (static_cast<uint32_t>(D >> 3) << 17);
-    const uint32_t q_at = smem_u32(smem), k_at = q_at + S::kOffK, v_at = q_at + S::kOffV;
-    // the issuing thread's two products; false when a wait gave up
-    auto product_s = [&](int r, int j) {  // scores = q * keys of tile j
-      if (!wait_bounded(bar(ctl->k_full[j % kStages]), (j / kStages) & 1, ctl, a.err)) return false;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t k = k_at + (j % kStages) * S::kK, q = q_at + r * S::kQ;
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x)
-        umma_ss(s_col(r), sw128_desc(q + (x / 4) * kHalf + 32 * (x & 3)),
-                sw128_desc(k + (x / 4) * kHalf + 32 * (x & 3)), kIdescS, x > 0);
-      umma_commit(bar(ctl->s_full[r]));
-      umma_commit(bar(ctl->k_empty[j % kStages]));
-      return true;
-    };
-    auto product_o = [&](int r, int j) {  // sums += weights of tile j * values
-      if (!wait_bounded(bar(ctl->v_full[j % kStages]), (j / kStages) & 1, ctl, a.err)) return false;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t v = v_at + (j % kStages) * S::kV;
-#pragma unroll
-      for (int k = 0; k < TK / 16; ++k)
-        umma_ts(o_col(r), s_col(r) + 8 * k, sw128_desc(v + (k / 4) * (D * 128) + 32 * (k & 3)),
-                kIdescO, j > 0 || k > 0);
-      umma_commit(bar(ctl->v_empty[j % kStages]));
-      return true;
-    };
     const int r = warp >> 2;
     if (r < nr) {
       const int row = static_cast<int>(threadIdx.x);  // of the CTA's 256
@@ -319,25 +331,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
       {  // q, in the stored order, as fp16
         const uint16_t* src = a.q + (static_cast<int64_t>(sp.q0) + i) * a.q_ts +
                               (static_cast<int64_t>(h) * a.group + hh) * a.q_hs;
-        uint4 x[D / 8];
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          x[c] = make_uint4(0, 0, 0, 0);
+        auto chunk = [&](int c) {  // stored places 8 c ..
+          uint4 x = make_uint4(0, 0, 0, 0);
           if (real) {
             if constexpr (BS >= 64) {
-              x[c] = __ldg(reinterpret_cast<const uint4*>(src + value_at<D, BS>(8 * c)));
+              x = __ldg(reinterpret_cast<const uint4*>(src + value_at<D, BS>(8 * c)));
             } else {
               const uint2 y0 = __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c)));
               const uint2 y1 =
                   __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c + 4)));
-              x[c] = make_uint4(y0.x, y0.y, y1.x, y1.y);
+              x = make_uint4(y0.x, y0.y, y1.x, y1.y);
             }
           }
-          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          return x;
+        };
+        uint32_t top = 0;  // first the row's largest, then its values (from the cache)
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 x = chunk(c);
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            top = max(top, max(w[y] & 0x7fffu, (w[y] >> 16) & 0x7fffu));
+          for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, (y[e] >> 16) & 0x7fffu));
         }
         float f = 1.0f;
         if constexpr (F == BNB4_BF16) {
@@ -349,9 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         if (top >= (F == BNB4_BF16 ? 0x7f80u : 0x7c00u)) qs = __int_as_float(0x7fffffff);
         qs *= a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale;
         uint8_t* dst = smem + r * S::kQ + (row & (TR - 1)) * 128;
-#pragma unroll
+#pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
-          uint4 y = x[c];
+          uint4 y = chunk(c);
           if constexpr (F == BNB4_BF16)
             y = make_uint4(pack_f16x2(bf16_lo(y.x) * f, bf16_hi(y.x) * f),
                            pack_f16x2(bf16_lo(y.y) * f, bf16_hi(y.y) * f),
@@ -360,10 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           *reinterpret_cast<uint4*>(dst + (c / 8) * kHalf + (((c & 7) ^ (row & 7)) << 4)) = y;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        group_sync(3 + r);  // all of the row tile's q is there
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ctl->q_full[r]));
       }
-      const bool issuer = (threadIdx.x & (TR - 1)) == 0;
-      if (issuer && T > 0) product_s(r, 0);  // a wait that gives up ends the others, too
       // what this row sees, and what all rows of the row tile see
       const int pos = sp.first + rr / a.group;
       const int see_hi = !real ? -1 : a.causal && pos < sp.len ? pos : sp.len - 1;
@@ -375,113 +388,101 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
 
       float m = -INFINITY, l = 0.0f;
       int ve = 0;
-      bool ok = true;
-      for (int j = 0; j < T; ++j) {
-        // (the group's warps meet below: they leave together)
-        if (!group_all(3 + r, warp_wait(ctl->s_full[r], j & 1) &&
-                                  warp_wait(ctl->m_full[j % kRing], (j / kRing) & 1))) {
-          ok = false;
-          break;
-        }
+      for (int i2 = 0; i2 < 2 * T; ++i2) {
+        const int j = i2 >> 1, hf = i2 & 1;
+        if (hf == 0) warp_wait(ctl->m_full[j % kRing], (j / kRing) & 1);
+        warp_wait(ctl->s_full[r][hf], j & 1);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t at = s_col(r) + lanes + TH * hf;
         const Meta& mt = ctl->meta[j % kRing];
-        const uint32_t present = *reinterpret_cast<const uint32_t*>(mt.present);
+        // a bit per 16 tokens of the half
+        const uint32_t pr = *reinterpret_cast<const uint16_t*>(mt.present + 2 * hf);
+        const uint32_t present = (pr & 3u) | ((pr >> 6) & 12u);
         const int tve = mt.value_exp;
-        const float q2 = qs * pow2(mt.key_exp);
-        const int j0 = sp.base + (tile0 + j) * TK;
-        const bool masked =
-            present != 0x03030303u || j0 < all_lo || j0 + TK - 1 > all_hi;  // warp-uniform
-        // columns lo .. hi of the tile are inside what the row sees
+        float q2 = qs * pow2(mt.key_exp);
+        if (q2 == 0.0f) q2 = 0x1p-126f;  // so that -infinity stays masked
+        const int j0 = sp.base + (tile0 + j) * TK + TH * hf;
+        const bool masked = present != 15u || j0 < all_lo || j0 + TH - 1 > all_hi;  // warp-uniform
+        // columns lo .. hi of the half are inside what the row sees
         const int lo = see_lo - j0, hi = see_hi - j0;
-        float v[32];
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < TK / 32; ++c) {
-          tmem_load32(s_col(r) + lanes + 32 * c, v);
-          if (masked) {
-            const uint32_t here = present >> (8 * c);
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((here >> (x / 16)) & 1u) || 32 * c + x < lo || 32 * c + x > hi)
-                v[x] = -INFINITY;
-          }
-          float t0 = v[0], t1 = v[1];
-#pragma unroll
-          for (int x = 2; x < 32; x += 2) t0 = fmaxf(t0, v[x]), t1 = fmaxf(t1, v[x + 1]);
-          top = fmaxf(top, fmaxf(t0, t1));
+        float v[32], w[32];
+        tmem_load32(at, v);
+        tmem_load32(at + 32, w);
+        tmem_load_done(v);
+        tmem_load_done(w);
+        if (masked) {
+          mask32(v, present, lo, hi);
+          mask32(w, present >> 2, lo - 32, hi - 32);
         }
-        top *= q2;  // q2 > 0, or NaN (which the comparisons below ignore)
+        float t0 = fmaxf(v[0], w[0]), t1 = fmaxf(v[1], w[1]);
+#pragma unroll
+        for (int x = 2; x < 32; x += 2) {
+          t0 = fmaxf(t0, fmaxf(v[x], w[x]));
+          t1 = fmaxf(t1, fmaxf(v[x + 1], w[x + 1]));
+        }
+        // q2 > 0, or NaN (which the comparisons below ignore)
+        const float top = fmaxf(t0, t1) * q2;
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
-        const bool shift = j > 0 && tve != ve;
+        const bool shift = i2 > 0 && tve != ve;
         if (__any_sync(0xffffffffu, grow) || shift) {
           const float old = m;
           if (grow) m = top;
           float f = grow ? ex2(old - m) : 1.0f;
           l *= f;
           if (shift) f *= ve - tve < -126 ? 0.0f : pow2(ve - tve);
-          if (j > 0) {
+          if (i2 > 0) {
+            // the sums so far, once they are complete: the scores asked for
+            // after them are (if any were), or they themselves
+            if (i2 + 1 < 2 * T)
+              warp_wait(ctl->s_full[r][hf ^ 1], ((i2 + 1) >> 1) & 1);
+            else
+              warp_wait(ctl->o_full[r], 0);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t y[16];
+              tmem_load16(o_col(r) + lanes + 16 * c, y);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              tmem_load32(o_col(r) + lanes + 32 * c, v);
-#pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] *= f;
-              tmem_store32(o_col(r) + lanes + 32 * c, v);
+              for (int x = 0; x < 16; ++x) y[x] = __float_as_uint(__uint_as_float(y[x]) * f);
+              tmem_store16(o_col(r) + lanes + 16 * c, y);
             }
           }
         }
         ve = tve;
         const float ref = (m == -INFINITY ? 0.0f : m) - static_cast<float>(kBoost);
         float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < TK / 32; ++c) {
-          tmem_load32(s_col(r) + lanes + 32 * c, v);
-          uint32_t p[16];
+        uint32_t p[16];
+        auto weights = [&](float (&y)[32]) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] = ex2(fmaf(v[x], q2, -ref));
-          if (masked) {
-            const uint32_t here = present >> (8 * c);
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((here >> (x / 16)) & 1u) || 32 * c + x < lo || 32 * c + x > hi) v[x] = 0.0f;
+          for (int x = 0; x < 32; x += 2) {
+            y[x] = ex2(fmaf(y[x], q2, -ref));
+            y[x + 1] = ex2(fmaf(y[x + 1], q2, -ref));
+            l0 += y[x];
+            l1 += y[x + 1];
+            p[x / 2] = pack_f16x2(y[x], y[x + 1]);
           }
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            l0 += v[2 * x];
-            l1 += v[2 * x + 1];
-            p[x] = pack_f16x2(v[2 * x], v[2 * x + 1]);
-          }
-          tmem_store16(s_col(r) + lanes + 16 * c, p);
-        }
+        };
+        weights(v);
+        tmem_store16(at, p);
+        weights(w);
+        tmem_store16(at + 16, p);
         l += l0 + l1;
         // a value that is not finite, of a token that this row sees
-        if ((mt.bad[0] | mt.bad[1] | mt.bad[2] | mt.bad[3]) != 0)
-          for (int x = 0; x < TK; ++x)
-            if ((mt.bad[x >> 5] >> (x & 31)) & 1u)
+        if ((mt.bad[2 * hf] | mt.bad[2 * hf + 1]) != 0)
+          for (int x = 0; x < TH; ++x)
+            if ((mt.bad[2 * hf + (x >> 5)] >> (x & 31)) & 1u)
               if (x >= lo && x <= hi) l = __int_as_float(0x7fffffff);
         tmem_store_done();
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        group_sync(3 + r);  // all of the row tile's weights are there
-        if (issuer) {
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (product_o(r, j)) {
-            if (j + 1 < T)
-              product_s(r, j + 1);
-            else
-              umma_commit(bar(ctl->o_full[r]));
-          }
-        }
         __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ctl->p_full[r][hf]));
       }
       // ---------------------------------------------------------- output
-      if (!ok && issuer) {  // products in flight finish before tensor memory is given back
-        umma_commit(bar(ctl->o_full[r]));
-        wait_drain(bar(ctl->o_full[r]), 0, ctl);
-      }
-      if (ok && T > 0) {
-        ok = warp_wait(ctl->o_full[r], 0);
+      if (T > 0) {
+        warp_wait(ctl->done[r], 0);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       }
-      if (ok) {  // warp-uniform
+      {
         const float back = pow2(ve - value_top(a.qtype)) *
                            (a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale);
         const float lse_top = m - static_cast<float>(kBoost);
@@ -498,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             tmem_load32(o_col(r) + lanes + 32 * c, v);
+            tmem_load_done(v);
             if (real) {
 #pragma unroll
               for (int x = 0; x < 32; x += 8) {
@@ -528,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           for (int c = 0; c < D / 32; ++c) {
             if (T > 0) {  // CTA-uniform
               tmem_load32(o_col(r) + lanes + 32 * c, v);
+              tmem_load_done(v);
               if (real) {
 #pragma unroll
                 for (int x = 0; x < 32; x += 4)
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         }
       }
     }
-  } else {
+  } else if (warp < kIssueWarp) {
     // ------------------------------------------- keys and values: decode
     const bool values = warp >= kValueWarp;
     const int u = static_cast<int>(threadIdx.x) - (values ? kValueWarp : kKeyWarp) * 32;
@@ -661,57 +664,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
       }
       // the products that read this stage last have completed; all of the
       // group's scales are there
-      if (!group_all(values ? 2 : 1, warp_wait(values ? ctl->v_empty[s] : ctl->k_empty[s],
-                                               ((j / kStages) & 1) ^ 1)))
-        break;
+      warp_wait(values ? ctl->v_empty[s] : ctl->k_empty[s], ((j / kStages) & 1) ^ 1);
+      group_sync(values ? 2 : 1);
       if (!values) {
         uint8_t* dst = smem + S::kOffK + s * S::kK + u * 128;
+#pragma unroll 1
+        for (int x0 = 0; x0 < kWords; x0 += 4) {
 #pragma unroll
-        for (int x = 0; x < kWords; ++x) {
-          const uint4 y = make_uint4(pair_of<0>(w[x], lane_table), pair_of<1>(w[x], lane_table),
-                                     pair_of<2>(w[x], lane_table), pair_of<3>(w[x], lane_table));
-          // word x holds stored places 8 x ..: of one block, or two of 4 values
-          const int b0 = ((8 * x) % (D / 8)) / (BS / 8);
-          const int b1 = ((8 * x + 4) % (D / 8)) / (BS / 8);
-          *reinterpret_cast<uint4*>(dst + (x / 8) * kHalf + (((x & 7) ^ (u & 7)) << 4)) =
-              make_uint4(mul_f16x2(y.x, fac[b0]), mul_f16x2(y.y, fac[b0]),
-                         mul_f16x2(y.z, fac[b1]), mul_f16x2(y.w, fac[b1]));
+          for (int y = 0; y < 4; ++y) {
+            const uint4 v = make_uint4(pair_of<0>(w[y], lane_table), pair_of<1>(w[y], lane_table),
+                                       pair_of<2>(w[y], lane_table), pair_of<3>(w[y], lane_table));
+            // word x0 + y holds stored places 8 (x0 + y) ..: of one block, or two of
+            // 4 values; 4 words are whole strips, so the blocks follow from y
+            const int b0 = ((8 * y) % (D / 8)) / (BS / 8), b1 = ((8 * y + 4) % (D / 8)) / (BS / 8);
+            *reinterpret_cast<uint4*>(dst + (x0 / 8) * kHalf + ((((x0 & 7) + y) ^ (u & 7)) << 4)) =
+                make_uint4(mul_f16x2(v.x, fac[b0]), mul_f16x2(v.y, fac[b0]),
+                           mul_f16x2(v.z, fac[b1]), mul_f16x2(v.w, fac[b1]));
+          }
+#pragma unroll
+          for (int y = 0; y < 12; ++y) w[y] = w[y + 4];
         }
       } else {
         // the 8 tokens are piece group % 8 of half group / 8 of the operand's rows
         uint8_t* half = smem + S::kOffV + s * S::kV + (group / 8) * (D * 128);
-#pragma unroll
-        for (int x = 0; x < kUnits; ++x) {
-          const int word = word0 + x;
+#pragma unroll 1
+        for (int word = word0; word < word0 + kUnits; ++word) {
           // bytes of two tokens' codes: of the word's even values, and its odd ones
           uint32_t ev[4], od[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const uint32_t t0 = w[8 * x + 2 * y], t1 = w[8 * x + 2 * y + 1];
+            const uint32_t t0 = w[2 * y], t1 = w[2 * y + 1];
             ev[y] = (t0 & 0xf0f0f0f0u) | ((t1 >> 4) & 0x0f0f0f0fu);
             od[y] = ((t0 << 4) & 0xf0f0f0f0u) | (t1 & 0x0f0f0f0fu);
           }
+#pragma unroll
+          for (int y = 0; y < 8; ++y) w[y] = w[y + 8];
           const int b0 = ((8 * word) % (D / 8)) / (BS / 8);
-          const int b1 = ((8 * word + 4) % (D / 8)) / (BS / 8);
-          const uint4 g0 = *reinterpret_cast<const uint4*>(&value_scale[b0][8 * group]);
-          const uint4 g1 =
-              BS == 32 ? *reinterpret_cast<const uint4*>(&value_scale[b1][8 * group]) : g0;
-          auto row_out = [&](int y, uint32_t p0, uint32_t p1, uint32_t p2, uint32_t p3) {
-            const uint4 g = y < 4 ? g0 : g1;
-            *reinterpret_cast<uint4*>(half + (8 * word + y) * 128 + (((group & 7) ^ y) << 4)) =
-                make_uint4(mul_f16x2(p0, g.x), mul_f16x2(p1, g.y), mul_f16x2(p2, g.z),
-                           mul_f16x2(p3, g.w));
-          };
-#define BNB4_VALUE_ROWS(I)                                                                   \
-  row_out(2 * I, pair_of<I>(ev[0], lane_table), pair_of<I>(ev[1], lane_table),               \
-          pair_of<I>(ev[2], lane_table), pair_of<I>(ev[3], lane_table));                     \
-  row_out(2 * I + 1, pair_of<I>(od[0], lane_table), pair_of<I>(od[1], lane_table),           \
-          pair_of<I>(od[2], lane_table), pair_of<I>(od[3], lane_table));
-          BNB4_VALUE_ROWS(0)
-          BNB4_VALUE_ROWS(1)
-          BNB4_VALUE_ROWS(2)
-          BNB4_VALUE_ROWS(3)
-#undef BNB4_VALUE_ROWS
+          uint4 g = *reinterpret_cast<const uint4*>(&value_scale[b0][8 * group]);
+          uint8_t* dst = half + 8 * word * 128;
+#pragma unroll 1
+          for (int y = 0; y < 8; y += 2) {  // values 8 word + y and the next: byte y / 2
+            if (BS == 32 && y == 4)
+              g = *reinterpret_cast<const uint4*>(&value_scale[b0 + 1][8 * group]);
+            *reinterpret_cast<uint4*>(dst + y * 128 + (((group & 7) ^ y) << 4)) = make_uint4(
+                mul_f16x2(pair_of<0>(ev[0], lane_table), g.x),
+                mul_f16x2(pair_of<0>(ev[1], lane_table), g.y),
+                mul_f16x2(pair_of<0>(ev[2], lane_table), g.z),
+                mul_f16x2(pair_of<0>(ev[3], lane_table), g.w));
+            *reinterpret_cast<uint4*>(dst + (y + 1) * 128 + (((group & 7) ^ (y + 1)) << 4)) =
+                make_uint4(mul_f16x2(pair_of<0>(od[0], lane_table), g.x),
+                           mul_f16x2(pair_of<0>(od[1], lane_table), g.y),
+                           mul_f16x2(pair_of<0>(od[2], lane_table), g.z),
+                           mul_f16x2(pair_of<0>(od[3], lane_table), g.w));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) ev[x] >>= 8, od[x] >>= 8;
+          }
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -722,6 +729,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
       for (int x = 0; x < NB; ++x) sc[x] = scn[x];
 #pragma unroll
       for (int x = 0; x < 16; ++x) w[x] = wn[x];
+    }
+  } else {
+    // ------------------------------------------------------- products
+    constexpr uint32_t kBase = (1u << 4) | (static_cast<uint32_t>(TR >> 4) << 24);
+    constexpr uint32_t kIdescS = kBase | (static_cast<uint32_t>(TH >> 3) << 17);
+    constexpr uint32_t kIdescO = kBase | (static_cast<uint32_t>(D >> 3) << 17);
+    const uint32_t q_at = smem_u32(smem), k_at = q_at + S::kOffK, v_at = q_at + S::kOffV;
+    // A wait that gives up ends every later one at once, and all loops run on
+    // to their end on whatever is there.
+    const int r = warp - kIssueWarp;
+    const uint32_t one = lane == 0 ? 1u : 0u;
+    const uint32_t q_lo = desc_lo(q_at + r * S::kQ), k_lo = desc_lo(k_at), v_lo = desc_lo(v_at);
+    auto product_s = [&](int i) {  // scores = q * keys: half i & 1 of tile i / 2
+      const int j = i >> 1, hf = i & 1;
+      if (hf == 0) warp_wait(ctl->k_full[j % kStages], (j / kStages) & 1);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t k = k_lo + (j % kStages) * (S::kK / 16) + hf * (TH * 128 / 16);
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+        umma_ss(one, s_col(r) + TH * hf, q_lo + (x / 4) * (kHalf / 16) + 2 * (x & 3),
+                k + (x / 4) * (kHalf / 16) + 2 * (x & 3), kIdescS, x > 0);
+      umma_commit(one, bar(ctl->s_full[r][hf]));
+      if (hf) umma_commit(one, bar(ctl->k_empty[j % kStages]));
+    };
+    auto product_o = [&](int i) {  // sums += weights * values
+      const int j = i >> 1, hf = i & 1;
+      if (hf == 0) warp_wait(ctl->v_full[j % kStages], (j / kStages) & 1);
+      warp_wait(ctl->p_full[r][hf], j & 1);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t v = v_lo + (j % kStages) * (S::kV / 16) + hf * (D * 128 / 16);
+#pragma unroll
+      for (int k = 0; k < TH / 16; ++k)
+        umma_ts(one, o_col(r), s_col(r) + TH * hf + 8 * k, v + 2 * k, kIdescO, i > 0 || k > 0);
+      if (hf) umma_commit(one, bar(ctl->v_empty[j % kStages]));
+    };
+    if (r < nr && T > 0) {
+      warp_wait(ctl->q_full[r], 0);
+      product_s(0);
+      product_s(1);
+      for (int i = 0; i < 2 * T; ++i) {
+        product_o(i);
+        if (i + 2 < 2 * T)
+          product_s(i + 2);
+        else
+          umma_commit(one, bar(i + 1 < 2 * T ? ctl->o_full[r] : ctl->done[r]));
+      }
+      // after a wait that gave up the products in flight still finish before
+      // tensor memory is given back
+      if (lane == 0 && *reinterpret_cast<volatile int*>(&ctl->abort))
+        wait_drain(bar(ctl->done[r]), 0, ctl);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
