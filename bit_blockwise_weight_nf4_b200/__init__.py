@@ -454,23 +454,20 @@ def gemv_4bit_grouped(items, outs=None, _persistent=False):
 
 
 # --------------------------------------------------- key/value cache (torch)
-class _On:
-    """The device a call's tensors live on, made current while it runs."""
-
-    def __init__(self, device):
-        _need(device.type == "cuda", "the cache is not on a CUDA device")
-        self.cuda = _torch().cuda
-        self.device = device.index
-
-    def __enter__(self):
-        self.back = self.cuda.current_device()
-        if self.device != self.back:
-            self.cuda.set_device(self.device)
-        return self.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.device != self.back:
-            self.cuda.set_device(self.back)
+# A decoder makes these calls once per layer and step, so the checks are
+# written to cost little: each tensor's shape and strides are fetched once,
+# and what failed is only worked out when something did.
+def _on(device, call):
+    """``call(stream)`` with the device (an index) current, on its current
+    stream."""
+    torch = _torch()
+    if device < 0:
+        raise ValueError("the cache is not on a CUDA device")
+    C = torch._C
+    if C._cuda_getDevice() == device:
+        return call(C._cuda_getCurrentRawStream(device))
+    with torch.cuda.device(device):
+        return call(C._cuda_getCurrentRawStream(device))
 
 
 def _need(ok, what):
@@ -488,26 +485,27 @@ class KVCache4bit:
 
     def __init__(self, k_codes, v_codes, k_absmax, v_absmax, blocksize=64, qtype=NF4):
         torch = _torch()
-        _need(k_codes.dim() == 4 and k_codes.dtype == torch.uint8,
+        shape, dtype, index = k_codes.shape, k_absmax.dtype, k_codes.get_device()
+        _need(len(shape) == 4 and k_codes.dtype == torch.uint8,
               "codes are uint8 [pages, kv heads, page size, D / 2]")
-        pages, heads, page, half = k_codes.shape
-        dt = {torch.bfloat16: BF16, torch.float16: F16}.get(k_absmax.dtype)
+        pages, heads, page, half = shape
+        dt = BF16 if dtype == torch.bfloat16 else F16 if dtype == torch.float16 else None
         if dt is None:
             raise TypeError("a cache's scales are bfloat16 or float16")
-        _need(v_codes.shape == k_codes.shape and v_codes.dtype == torch.uint8,
+        _need(v_codes.shape == shape and v_codes.dtype == torch.uint8,
               "k_codes and v_codes differ in shape or dtype")
         _need(blocksize > 0 and k_absmax.shape == (pages, heads, page, 2 * half // blocksize),
               "k_absmax is [pages, kv heads, page size, D / blocksize]")
-        _need(v_absmax.shape == k_absmax.shape and v_absmax.dtype == k_absmax.dtype,
+        _need(v_absmax.shape == k_absmax.shape and v_absmax.dtype == dtype,
               "k_absmax and v_absmax differ in shape or dtype")
         for t in (k_codes, v_codes, k_absmax, v_absmax):
-            _need(t.is_contiguous() and t.device == k_codes.device,
+            _need(t.is_contiguous() and t.get_device() == index,
                   "a cache's tensors are contiguous and on one device")
         self.k_codes, self.v_codes = k_codes, v_codes
         self.k_absmax, self.v_absmax = k_absmax, v_absmax
         self.num_pages, self.n_kv_heads, self.page_size = pages, heads, page
         self.head_dim, self.blocksize, self.qtype = 2 * half, blocksize, qtype
-        self.dtype, self.device = k_absmax.dtype, k_codes.device
+        self.dtype, self.device_index, self.dtype_code = dtype, index, dt
         self.struct = KvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_absmax.data_ptr(),
                               v_absmax.data_ptr(), pages, page, heads, 2 * half, blocksize,
                               qtype, dt, 0)
@@ -525,26 +523,37 @@ class KVCache4bit:
         return KVCache4bit(*codes, *scales, blocksize, qtype)
 
     @property
+    def device(self):
+        return self.k_codes.device
+
+    @property
     def nbytes(self):
         return sum(t.numel() * t.element_size()
                    for t in (self.k_codes, self.v_codes, self.k_absmax, self.v_absmax))
 
 
-def _kv_rows(t, cache, tokens, what):
-    """(pointer, token stride, head stride) of k, v, q or out [T, H, D]."""
-    _need(t.dim() == 3 and t.shape[0] == tokens and t.shape[2] == cache.head_dim
-          and (t.stride(2) == 1 or t.numel() == 0),
-          "%s is [tokens, heads, %d] with a contiguous last dimension" % (what, cache.head_dim))
-    _need(t.device == cache.device, "%s is on another device than the cache" % what)
+def _kv_rows(t, cache, tokens, heads, what):
+    """(pointer, token stride, head stride) of k, v, q or out [T, H, D]; any
+    number of heads where ``heads`` is None."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != cache.head_dim or \
+            (heads is not None and shape[1] != heads) or \
+            (stride[2] != 1 and tokens * shape[1] > 0):
+        raise ValueError("%s is [tokens, heads, %d] with a contiguous last dimension, and has the "
+                         "cache's (or the queries') heads" % (what, cache.head_dim))
+    if t.get_device() != cache.device_index:
+        raise ValueError("%s is on another device than the cache" % what)
     # the stride of a dimension of one is never used, and may be anything
-    return (t.data_ptr(), t.stride(0) if tokens > 1 else 0,
-            t.stride(1) if t.shape[1] > 1 else 0)
+    return (t.data_ptr(), stride[0] if tokens > 1 else 0, stride[1] if shape[1] > 1 else 0)
 
 
-def _index(t, cache, dtype, what):
-    _need(t.dtype == dtype and t.device == cache.device,
-          "%s is a %s tensor on the cache's device" % (what, dtype))
-    return t
+def _index(t, cache, dtype, shape, what):
+    """The pointer of a contiguous index tensor."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or \
+            t.get_device() != cache.device_index:
+        raise ValueError("%s is a contiguous %s tensor %s on the cache's device"
+                         % (what, dtype, list(shape)))
+    return t.data_ptr()
 
 
 def kv_write_4bit(k, v, cache, slots):
@@ -555,13 +564,11 @@ def kv_write_4bit(k, v, cache, slots):
     torch = _torch()
     T = k.shape[0]
     _need(k.dtype == cache.dtype and v.dtype == cache.dtype, "k and v have the cache's dtype")
-    kr, vr = _kv_rows(k, cache, T, "k"), _kv_rows(v, cache, T, "v")
-    _need(k.shape[1] == cache.n_kv_heads and v.shape[1] == cache.n_kv_heads,
-          "k and v have the cache's heads")
-    _index(slots, cache, torch.int64, "slots")
-    _need(slots.shape == (T,) and slots.is_contiguous(), "slots is a contiguous [T]")
-    with _On(cache.device) as stream:
-        rc = bnb_kv_write_4bit(*kr, *vr, T, slots.data_ptr(), cache.struct, stream)
+    kp, kt, kh = _kv_rows(k, cache, T, cache.n_kv_heads, "k")
+    vp, vt, vh = _kv_rows(v, cache, T, cache.n_kv_heads, "v")
+    sp = _index(slots, cache, torch.int64, (T,), "slots")
+    rc = _on(cache.device_index, lambda stream: bnb_kv_write_4bit(
+        kp, kt, kh, vp, vt, vh, T, sp, cache.struct, stream))
     _check(rc, "bnb_kv_write_4bit")
     return cache
 
@@ -572,30 +579,27 @@ def kv_read_4bit(cache, slots, out_dtype=None, out=None):
     dtype), or into ``out`` = (k, v), either of which may be None.  Rows of a
     slot outside the cache are not written."""
     torch = _torch()
-    _index(slots, cache, torch.int64, "slots")
-    _need(slots.dim() == 1 and slots.is_contiguous(), "slots is a contiguous [T]")
-    T = slots.shape[0]
+    T, H, D = slots.shape[0], cache.n_kv_heads, cache.head_dim
+    sp = _index(slots, cache, torch.int64, (T,), "slots")
     if out is None:
-        kv = torch.empty(2, T, cache.n_kv_heads, cache.head_dim, dtype=out_dtype or cache.dtype,
-                         device=cache.device)
-        out = kv[0], kv[1]
-    k, v = out
-    dt = None
-    rows = []
-    for t in (k, v):
-        if t is None:
-            rows += [None, 0, 0]
-            continue
-        d = _DT.get(str(t.dtype))
-        if d is None or (dt is not None and d != dt):
-            raise TypeError("kv_read_4bit writes float32, bfloat16 or float16")
-        dt = d
-        _need(t.shape[1] == cache.n_kv_heads, "out has the cache's heads")
-        rows += _kv_rows(t, cache, T, "out")
+        kv = torch.empty((2, T, H, D), dtype=out_dtype or cache.dtype, device=slots.device)
+        k, v = kv.unbind(0)
+        dt = cache.dtype_code if out_dtype is None else _DT.get(str(out_dtype))
+        p = kv.data_ptr()
+        rows = (p, H * D, D, p + kv.element_size() * T * H * D, H * D, D)
+    else:
+        k, v = out
+        _need(k is not None or v is not None, "kv_read_4bit: neither k nor v asked for")
+        some = k if k is not None else v
+        dt = _DT.get(str(some.dtype))
+        if k is not None and v is not None and k.dtype != v.dtype:
+            dt = None
+        rows = (() if k is None else _kv_rows(k, cache, T, H, "out")) or (None, 0, 0)
+        rows += (() if v is None else _kv_rows(v, cache, T, H, "out")) or (None, 0, 0)
     if dt is None:
-        raise ValueError("kv_read_4bit: neither k nor v asked for")
-    with _On(cache.device) as stream:
-        rc = bnb_kv_read_4bit(cache.struct, slots.data_ptr(), T, *rows, dt, stream)
+        raise TypeError("kv_read_4bit writes float32, bfloat16 or float16 (one of them)")
+    rc = _on(cache.device_index, lambda stream: bnb_kv_read_4bit(
+        cache.struct, sp, T, *rows, dt, stream))
     _check(rc, "bnb_kv_read_4bit")
     return k, v
 
@@ -613,47 +617,41 @@ def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None
     ``max_seq_len`` (default: what the block table holds) is the bound by
     which the work is split."""
     torch = _torch()
-    T = q.shape[0]
+    i32 = torch.int32
+    T, heads = q.shape[0], q.shape[1]
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     _need(q.dtype == cache.dtype and out.dtype == cache.dtype, "q and out have the cache's dtype")
-    qr, outr = _kv_rows(q, cache, T, "q"), _kv_rows(out, cache, T, "out")
-    heads = q.shape[1]
-    _need(out.shape[1] == heads, "out has another number of heads than q")
-    _index(block_table, cache, torch.int32, "block_table")
-    _index(seq_lens, cache, torch.int32, "seq_lens")
-    _need(block_table.dim() == 2 and block_table.stride(1) == 1 or block_table.shape[-1] == 1,
-          "block_table is [B, W] with contiguous rows")
-    B, W = block_table.shape
-    _need(seq_lens.shape == (B,) and seq_lens.is_contiguous(), "seq_lens is a contiguous [B]")
+    qp, qt, qh = _kv_rows(q, cache, T, None, "q")
+    op, ot, oh = _kv_rows(out, cache, T, heads, "out")
+    table, step = block_table.shape, block_table.stride()
+    if len(table) != 2 or block_table.dtype != i32 or (step[1] != 1 and table[1] > 1) or \
+            block_table.get_device() != cache.device_index:
+        raise ValueError("block_table is int32 [B, W] with contiguous rows on the cache's device")
+    B, W = table
+    lens = _index(seq_lens, cache, i32, (B,), "seq_lens")
     if cu_seqlens_q is None:
-        _need(B > 0 and T % B == 0 or T == 0, "without cu_seqlens_q every sequence has T / B queries")
+        _need(T == 0 or (B > 0 and T % B == 0),
+              "without cu_seqlens_q every sequence has T / B queries")
         max_q_len = T // B if T else 1
         cu = None
     else:
-        _index(cu_seqlens_q, cache, torch.int32, "cu_seqlens_q")
-        _need(cu_seqlens_q.shape == (B + 1,) and cu_seqlens_q.is_contiguous(),
-              "cu_seqlens_q is a contiguous [B + 1]")
-        cu = cu_seqlens_q.data_ptr()
+        cu = _index(cu_seqlens_q, cache, i32, (B + 1,), "cu_seqlens_q")
         if max_q_len is None:
             max_q_len = max(1, T)
-    if lse is not None:
-        _index(lse, cache, torch.float32, "lse")
-        _need(lse.shape == (T, heads) and lse.is_contiguous(), "lse is a contiguous [T, heads]")
-    room = min(W * cache.page_size, 0x7fffffff)
-    a = Attn(*qr, *outr, None if lse is None else lse.data_ptr(),
-             ctypes.pointer(cache.struct), block_table.data_ptr(),
-             block_table.stride(0) if B > 1 else W, seq_lens.data_ptr(), cu, None, 0, T, B,
-             heads, max_q_len, room if max_seq_len is None else max_seq_len, W, int(bool(causal)),
-             window, cache.head_dim ** -0.5 if scale is None else scale, 0)
-    with _On(cache.device) as stream:
-        rc, size = bnb4_attn_workspace(a)
-        _check(rc, "bnb_attn_4bit")
-        if size:
-            if workspace is None:
-                workspace = torch.empty(size, dtype=torch.uint8, device=cache.device)
-            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-        rc = bnb_attn_4bit(a, stream)
+    lp = None if lse is None else _index(lse, cache, torch.float32, (T, heads), "lse")
+    if max_seq_len is None:
+        max_seq_len = min(W * cache.page_size, 0x7fffffff)
+    a = Attn(qp, qt, qh, op, ot, oh, lp, ctypes.pointer(cache.struct), block_table.data_ptr(),
+             step[0] if B > 1 else W, lens, cu, None, 0, T, B, heads, max_q_len, max_seq_len, W,
+             1 if causal else 0, window, cache.head_dim ** -0.5 if scale is None else scale, 0)
+    rc, size = bnb4_attn_workspace(a)
+    _check(rc, "bnb_attn_4bit")
+    if size:
+        if workspace is None:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    rc = _on(cache.device_index, lambda stream: bnb_attn_4bit(a, stream))
     _check(rc, "bnb_attn_4bit")
     return out
 

@@ -296,9 +296,9 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
     }
   }
   __syncthreads();
-  int b = 0, h = 0, rt = 0, tile0 = 0, left = 1;
+  int b = 0, h = 0, tile0 = 0, left = 1;
   int64_t item = run;
-  const int64_t items = static_cast<int64_t>(a.batch) * a.heads * a.row_tiles;
+  const int64_t items = static_cast<int64_t>(a.batch) * a.heads;
   if (a.split) {
     b = sm_item[grp][0], h = sm_item[grp][1], tile0 = sm_item[grp][2];
     left = sm_item[grp][3];
@@ -315,13 +315,11 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
       if (left <= 0 || b >= a.batch) break;
     } else {
       if (item >= items) break;
-      rt = static_cast<int>(item % a.row_tiles);
-      const int64_t x = item / a.row_tiles;
-      h = static_cast<int>(x % a.heads);
-      b = static_cast<int>(x / a.heads);
+      h = static_cast<int>(item % a.heads);
+      b = static_cast<int>(item / a.heads);
       item += runs;
     }
-    const Span sp = span_of<RT, TILE>(a, b, rt);
+    const Span sp = span_of<RT, TILE>(a, b, 0);
     if (sp.rows == 0) {  // uniform over the group
       if (a.split) ++b, h = 0, tile0 = 0;  // holds no tiles
       continue;
@@ -904,6 +902,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
 // ------------------------------------------------------------------- host
 constexpr int kMaxRuns = 320;  // bound of the runs, hence of the workspace
 
+// Whole pairs in turn where no pair has more than a tile per warp of a group
+// (a cut would only add the join), else the line of tiles cut into equal runs.
+template <int F, int NT, bool KR>
+constexpr int64_t unsplit_span() {
+  using S = Shape<128, 128, F, NT, KR>;  // the same for every head and block size
+  return S::TILE * S::GW;
+}
+
 template <int D, int BS, int F, int NT, bool KR>
 cudaError_t launch_t(AttnArgs& a, int64_t span, int num_sms, cudaStream_t s) {
   using S = Shape<D, BS, F, NT, KR>;
@@ -911,10 +917,8 @@ cudaError_t launch_t(AttnArgs& a, int64_t span, int num_sms, cudaStream_t s) {
   // shared memory to kEnd must be there (static and reserved bytes come off).
   constexpr int kSmem = static_cast<int>(S::kEnd);
   static_assert(kSmem + 4096 <= 232448, "shared memory budget");
-  // Whole pairs in turn where no pair has more than a tile per warp (a cut
-  // would only add the join), else the line of tiles cut into equal runs.
-  a.split = a.row_tiles == 1 && span > S::TILE * S::GW;
-  const int64_t items = static_cast<int64_t>(a.batch) * a.heads * a.row_tiles;
+  a.split = span > unsplit_span<F, NT, KR>();
+  const int64_t items = static_cast<int64_t>(a.batch) * a.heads;
   const int sms = num_sms < kMaxRuns / 2 ? num_sms : kMaxRuns / 2;
   const int grid = a.split || items > 2 * sms ? sms : static_cast<int>((items + 1) / 2);
   auto kern = attn_decode_kernel<D, BS, F, NT, KR>;
@@ -981,6 +985,10 @@ size_t attn_workspace_bytes(const bnb4_attn& p) {
   const AttnArgs a = args_of(p, &rows, &span);
   if (rows > kMaxRows) return attn_prefill_workspace(a, p.cache->head_dim, rows, span, kSms);
   const size_t rt = rows <= 8 ? 8 : 16;
+  const bool kr = p.cache->dtype == BNB4_F16 && p.cache->qtype == BNB4_NF4;
+  const int64_t whole = rows <= 8 ? (kr ? unsplit_span<BNB4_F16, 1, true>() : unsplit_span<BNB4_BF16, 1, false>())
+                                  : (kr ? unsplit_span<BNB4_F16, 2, true>() : unsplit_span<BNB4_BF16, 2, false>());
+  if (span <= whole) return 0;
   return sizeof(float) * 2 * kMaxRuns * rt * (static_cast<size_t>(p.cache->head_dim) + 2);
 }
 

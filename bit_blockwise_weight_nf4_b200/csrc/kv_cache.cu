@@ -16,9 +16,10 @@
 // Both kernels are bound by HBM: 2 D bytes of 16-bit values and D / 2 + 2 D /
 // BS bytes of cache per row.  A lane owns 8 values (16 bytes) of a row, so D
 // / 8 lanes hold a row and the block maximum is an xor-shuffle among BS / 8
-// of them; kRows rows are in flight per lane.  Table lookups are warp
-// shuffles (the table is one entry per lane: no shared memory to fill, which
-// a 16-token call would wait for): two per value to quantize, one to decode.
+// of them; kRows rows are in flight per lane, all of one token, whose slot is
+// looked up once.  Table lookups are warp shuffles (the table is one entry per
+// lane: no shared memory to fill, which a 16-token call would wait for): two
+// per value to quantize, one to decode.
 #include "common.cuh"
 #include "kvcache.h"
 
@@ -37,12 +38,13 @@ constexpr float kPerUnit = 14.4f;
 constexpr int kCenter = 15;
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 
-// {decision point (+inf: none), code below it | code above it << 8}; FP4's
-// negative points are stored as the float below, so that "v > point" decides
-// v >= -m (a tie goes to the smaller magnitude).
+// A bucket's decision point (+inf: none), the code below it, and what the point
+// adds to the code (NF4: one; FP4: the upper half of `codes`).  FP4's negative points are
+// stored as the float below, so that "v > point" decides v >= -m (a tie goes
+// to the smaller magnitude).
 struct Bucket {
   float point;
-  uint32_t codes;
+  int32_t codes;
 };
 
 __device__ __forceinline__ float midpoint(float a, float b) {
@@ -50,12 +52,12 @@ __device__ __forceinline__ float midpoint(float a, float b) {
 }
 
 __device__ Bucket bucket_of_lane(int qt, int lane) {
-  Bucket e{__int_as_float(0x7f800000), 0u};
+  Bucket e{__int_as_float(0x7f800000), 0};
   const float c = static_cast<float>(lane - kCenter) / kPerUnit;
   const float lo = c - 0.5f / kPerUnit - 1e-3f, hi = c + 0.5f / kPerUnit + 1e-3f;
   if (lane == 31) return e;
   if (qt == kQtNF4) {
-    uint32_t below = 0;
+    int below = 0;
 #pragma unroll
     for (int i = 0; i < 15; ++i) {
       const float m = midpoint(nf4_value(i), nf4_value(i + 1));
@@ -64,7 +66,7 @@ __device__ Bucket bucket_of_lane(int qt, int lane) {
       else if (m <= hi)
         e.point = m;
     }
-    e.codes = below | (below + 1) << 8;
+    e.codes = below;
   } else {
     // the magnitude of the bucket's end nearer zero, and whether a point is inside
     uint32_t m_lo = 0, m_hi = 0;  // magnitudes at the bucket's lower and upper end
@@ -77,18 +79,27 @@ __device__ Bucket bucket_of_lane(int qt, int lane) {
       if (m >= lo && m <= hi) e.point = m;
       if (-m >= lo && -m <= hi) e.point = __int_as_float(__float_as_int(-m) + 1);
     }
-    const uint32_t c_lo = lo < 0.0f && m_lo != 0 ? m_lo + 8u : m_lo;
-    const uint32_t c_hi = hi < 0.0f && m_hi != 0 ? m_hi + 8u : m_hi;
-    e.codes = c_lo | c_hi << 8;
+    const int c_lo = static_cast<int>(lo < 0.0f && m_lo != 0 ? m_lo + 8u : m_lo);
+    const int c_hi = static_cast<int>(hi < 0.0f && m_hi != 0 ? m_hi + 8u : m_hi);
+    e.codes = (c_hi - c_lo) * 65536 | c_lo;
   }
   return e;
 }
 
-__device__ __forceinline__ uint32_t code_of(float v, const Bucket& mine) {
+// codes * 16 + the code of v
+template <int QT>
+__device__ __forceinline__ uint32_t push_code(uint32_t codes, float v, const Bucket& mine) {
   const int j = __float_as_int(__fmaf_rn(v, kPerUnit, kMagic + kCenter));
   const float point = __shfl_sync(0xffffffffu, mine.point, j);
-  const uint32_t codes = __shfl_sync(0xffffffffu, mine.codes, j);
-  return (v > point ? codes >> 8 : codes) & 15u;
+  const int32_t c = __shfl_sync(0xffffffffu, mine.codes, j);
+  if constexpr (QT == kQtNF4) {
+    codes = codes * 16u + static_cast<uint32_t>(c);
+    if (v > point) ++codes;
+  } else {
+    codes = codes * 16u + static_cast<uint32_t>(c & 0xffff);
+    if (v > point) codes += static_cast<uint32_t>(c >> 16);
+  }
+  return codes;
 }
 
 // Where the 8 codes of values 8 c .. 8 c + 7 lie in a row: 4 bytes at `at`,
@@ -126,64 +137,58 @@ struct KvArgs {
   const int64_t* slots;
   uint8_t *k_codes, *v_codes;
   uint16_t *k_absmax, *v_absmax;
-  FastDiv per_token, page;  // 2 * heads, page size
-  uint32_t n_rows;          // tokens * 2 * heads
+  FastDiv per_token, page;  // units of a token; page size
+  uint32_t n_units;         // a unit: kRows rows of a token per lane
   int heads, qtype;
   int64_t n_slots;
 };
 
-// One lane's place: its row's token, K or V, head, and cache row (-1: the
-// token has no slot and is left out).
-struct Place {
+// A unit's token and its place in the cache: row 0 of its page's head 0 plus its
+// row in the page (rows of the next head are a page size on), or -1: the token
+// has no slot and is left out.
+struct Unit {
   uint32_t t;
-  int h;
-  bool v;
+  int x0;  // first of the token's 2 * heads rows: keys, then values
   int64_t row;
 };
-__device__ __forceinline__ Place place_of(const KvArgs& a, uint32_t r) {
-  Place p;
-  p.t = a.per_token.div(r);
-  const int x = static_cast<int>(r - p.t * a.per_token.d);
-  p.v = x >= a.heads;
-  p.h = p.v ? x - a.heads : x;
-  const int64_t slot = __ldg(a.slots + p.t);
-  p.row = -1;
+__device__ __forceinline__ Unit unit_of(const KvArgs& a, uint32_t u, int rows) {
+  Unit r;
+  r.t = a.per_token.div(u);
+  r.x0 = static_cast<int>(u - r.t * a.per_token.d) * rows;
+  const int64_t slot = __ldg(a.slots + r.t);
+  r.row = -1;
   if (slot >= 0 && slot < a.n_slots) {
     const uint32_t pg = a.page.div(static_cast<uint32_t>(slot));
-    p.row = (static_cast<int64_t>(pg) * a.heads + p.h) * a.page.d +
+    r.row = static_cast<int64_t>(pg) * a.heads * a.page.d +
             (static_cast<uint32_t>(slot) - pg * a.page.d);
   }
-  return p;
+  return r;
 }
 
-template <int D, int BS, int F>
+template <int D, int BS, int F, int QT>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvArgs a) {
   constexpr int LPR = D / 8;      // lanes per row
   constexpr int RPW = 32 / LPR;   // rows per warp and step
   constexpr int LPB = BS / 8;     // lanes per block
   pdl_trigger();
   const int lane = threadIdx.x & 31, c = lane % LPR;
-  const Bucket mine = bucket_of_lane(a.qtype, lane);
+  const Bucket mine = bucket_of_lane(QT, lane);
   pdl_wait();
   const uint32_t warps = gridDim.x * (kThreads / 32);
   const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  // 64-bit counters: the last step of a grid may pass n_rows
-  for (uint64_t r0 = static_cast<uint64_t>(warp) * RPW * kRows; r0 < a.n_rows;
-       r0 += static_cast<uint64_t>(warps) * RPW * kRows) {
+  for (uint32_t u = warp; u < a.n_units; u += warps) {
+    const Unit n = unit_of(a, u, RPW * kRows);
+    if (n.row < 0) continue;  // warp-uniform
     uint4 x[kRows];
-    Place p[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const uint64_t r = r0 + i * RPW + lane / LPR;
-      x[i] = make_uint4(0, 0, 0, 0);
-      p[i].row = -1;
-      if (r < a.n_rows) {
-        p[i] = place_of(a, static_cast<uint32_t>(r));
-        const int64_t at = p[i].v ? p[i].t * a.rows.v_ts + p[i].h * a.rows.v_hs
-                                  : p[i].t * a.rows.k_ts + p[i].h * a.rows.k_hs;
-        const uint16_t* src = static_cast<const uint16_t*>(p[i].v ? a.rows.v : a.rows.k);
-        if (p[i].row >= 0) x[i] = ldg_stream_v4(src + at + 8 * c);
-      }
+      const int r = n.x0 + i * RPW + lane / LPR;
+      const bool v = r >= a.heads;
+      const int h = v ? r - a.heads : r;
+      const uint16_t* src = static_cast<const uint16_t*>(v ? a.rows.v : a.rows.k);
+      const int64_t ts = v ? a.rows.v_ts : a.rows.k_ts, hs = v ? a.rows.v_hs : a.rows.k_hs;
+      x[i] = r < 2 * a.heads ? ldg_stream_v4(src + n.t * ts + h * hs + 8 * c)
+                             : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -191,8 +196,13 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvArgs a) {
       float e[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        e[2 * j] = half_to_f32<F>(F == BNB4_F16 ? w[j] & 0xffffu : w[j]);
-        e[2 * j + 1] = half_to_f32<F>(w[j] >> 16);
+        if constexpr (F == BNB4_BF16) {
+          e[2 * j] = bf16_lo(w[j]);
+          e[2 * j + 1] = bf16_hi(w[j]);
+        } else {
+          e[2 * j] = half_to_f32<F>(w[j] & 0xffffu);
+          e[2 * j + 1] = half_to_f32<F>(w[j] >> 16);
+        }
       }
       float m = 0.0f;
 #pragma unroll
@@ -200,24 +210,28 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvArgs a) {
 #pragma unroll
       for (int o = LPB / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float inv = m == 0.0f ? 0.0f : __frcp_rn(m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = __fmul_rn(e[j], inv);
+      // only a subnormal scale's reciprocal can leave [-1, 1] (or be
+      // infinite); every decision point is inside, and NaN stays NaN
+      if (__any_sync(0xffffffffu, m < 0x1p-120f)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = e[j] > 1.0f ? 1.0f : e[j] < -1.0f ? -1.0f : e[j];
+      }
       uint32_t codes = 0;
 #pragma unroll
       for (int j = 3; j >= 0; --j) {  // byte j = code[2 j] << 4 | code[2 j + 1]
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v = __fmul_rn(e[2 * j + h], inv);
-          // only a subnormal scale's reciprocal can leave [-1, 1] (or be
-          // infinite); every decision point is inside, and NaN stays NaN
-          if (m < 0x1p-120f) v = v > 1.0f ? 1.0f : v < -1.0f ? -1.0f : v;
-          codes = codes * 16u + code_of(v, mine);
-        }
+        codes = push_code<QT>(codes, e[2 * j], mine);
+        codes = push_code<QT>(codes, e[2 * j + 1], mine);
       }
-      if (p[i].row >= 0) {
-        store_codes<D, BS>((p[i].v ? a.v_codes : a.k_codes) + p[i].row * (D / 2), c, codes);
-        if (c % LPB == 0) {
-          uint16_t* s = (p[i].v ? a.v_absmax : a.k_absmax) + p[i].row * (D / BS) + c / LPB;
-          *s = static_cast<uint16_t>(pack2<F>(m, 0.0f));
-        }
+      const int r = n.x0 + i * RPW + lane / LPR;
+      if (r < 2 * a.heads) {
+        const bool v = r >= a.heads;
+        const int64_t row = n.row + static_cast<int64_t>(v ? r - a.heads : r) * a.page.d;
+        store_codes<D, BS>((v ? a.v_codes : a.k_codes) + row * (D / 2), c, codes);
+        if (c % LPB == 0)
+          (v ? a.v_absmax : a.k_absmax)[row * (D / BS) + c / LPB] =
+              static_cast<uint16_t>(pack2<F>(m, 0.0f));
       }
     }
   }
@@ -237,23 +251,19 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
   pdl_wait();
   const uint32_t warps = gridDim.x * (kThreads / 32);
   const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  for (uint64_t r0 = static_cast<uint64_t>(warp) * RPW * kRows; r0 < a.n_rows;
-       r0 += static_cast<uint64_t>(warps) * RPW * kRows) {
-    uint32_t w[kRows];
-    uint32_t s[kRows];
-    Place p[kRows];
+  for (uint32_t u = warp; u < a.n_units; u += warps) {
+    const Unit n = unit_of(a, u, RPW * kRows);
+    if (n.row < 0) continue;  // warp-uniform
+    uint32_t w[kRows], s[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const uint64_t r = r0 + i * RPW + lane / LPR;
+      const int r = n.x0 + i * RPW + lane / LPR;
+      const bool v = r >= a.heads;
+      const int64_t row = n.row + static_cast<int64_t>(v ? r - a.heads : r) * a.page.d;
       w[i] = s[i] = 0u;
-      p[i].row = -1;
-      if (r < a.n_rows) {
-        p[i] = place_of(a, static_cast<uint32_t>(r));
-        if ((p[i].v ? a.rows.v : a.rows.k) == nullptr) p[i].row = -1;  // not asked for
-      }
-      if (p[i].row >= 0) {
-        w[i] = load_codes<D, BS>((p[i].v ? a.v_codes : a.k_codes) + p[i].row * (D / 2), c);
-        s[i] = __ldg((p[i].v ? a.v_absmax : a.k_absmax) + p[i].row * (D / BS) + c / LPB);
+      if (r < 2 * a.heads) {
+        w[i] = load_codes<D, BS>((v ? a.v_codes : a.k_codes) + row * (D / 2), c);
+        s[i] = __ldg((v ? a.v_absmax : a.k_absmax) + row * (D / BS) + c / LPB);
       }
     }
 #pragma unroll
@@ -265,16 +275,19 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
         e[2 * j] = __fmul_rn(__shfl_sync(0xffffffffu, mine, w[i] >> (8 * j + 4)), m);
         e[2 * j + 1] = __fmul_rn(__shfl_sync(0xffffffffu, mine, w[i] >> (8 * j)), m);
       }
-      if (p[i].row < 0) continue;
-      const int64_t at = p[i].v ? p[i].t * a.rows.v_ts + p[i].h * a.rows.v_hs
-                                : p[i].t * a.rows.k_ts + p[i].h * a.rows.k_hs;
-      void* base = const_cast<void*>(p[i].v ? a.rows.v : a.rows.k);
+      const int r = n.x0 + i * RPW + lane / LPR;
+      const bool v = r >= a.heads;
+      const int h = v ? r - a.heads : r;
+      void* base = const_cast<void*>(v ? a.rows.v : a.rows.k);
+      if (r >= 2 * a.heads || base == nullptr) continue;  // null: not asked for
+      const int64_t at = n.t * (v ? a.rows.v_ts : a.rows.k_ts) +
+                         h * (v ? a.rows.v_hs : a.rows.k_hs) + 8 * c;
       if constexpr (OT == BNB4_F32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(base) + at + 8 * c);
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
         dst[0] = make_float4(e[0], e[1], e[2], e[3]);
         dst[1] = make_float4(e[4], e[5], e[6], e[7]);
       } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at + 8 * c) =
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) =
             make_uint4(pack2<OT>(e[0], e[1]), pack2<OT>(e[2], e[3]), pack2<OT>(e[4], e[5]),
                        pack2<OT>(e[6], e[7]));
       }
@@ -290,19 +303,21 @@ KvArgs args_of(const KvRows& rows, int64_t tokens, const int64_t* slots, const b
   a.v_codes = c.v_codes;
   a.k_absmax = static_cast<uint16_t*>(c.k_absmax);
   a.v_absmax = static_cast<uint16_t*>(c.v_absmax);
-  a.per_token = make_div(2u * static_cast<uint32_t>(c.n_kv_heads));
+  const int per_unit = 32 / (c.head_dim / 8) * kRows;
+  const int units = (2 * c.n_kv_heads + per_unit - 1) / per_unit;
+  a.per_token = make_div(static_cast<uint32_t>(units));
   a.page = make_div(static_cast<uint32_t>(c.page_size));
-  a.n_rows = static_cast<uint32_t>(tokens * 2 * c.n_kv_heads);
+  a.n_units = static_cast<uint32_t>(tokens * units);
   a.heads = c.n_kv_heads;
   a.qtype = c.qtype;
   a.n_slots = c.num_pages * c.page_size;
   return a;
 }
 
-// As many CTAs as the rows fill, 8 per SM at most (2048 threads).
-unsigned grid_for(const KvArgs& a, int head_dim, int num_sms) {
-  const int64_t rows_per_cta = static_cast<int64_t>(kThreads / (head_dim / 8)) * kRows;
-  const int64_t want = (a.n_rows + rows_per_cta - 1) / rows_per_cta;
+// As many CTAs as the units fill (a unit per warp), 8 per SM at most (2048
+// threads).
+unsigned grid_for(const KvArgs& a, int num_sms) {
+  const int64_t want = (static_cast<int64_t>(a.n_units) + kThreads / 32 - 1) / (kThreads / 32);
   const int64_t most = static_cast<int64_t>(num_sms) * 8;
   return static_cast<unsigned>(want < most ? want : most);
 }
@@ -321,12 +336,16 @@ unsigned grid_for(const KvArgs& a, int head_dim, int num_sms) {
 cudaError_t launch_kv_write(const KvRows& rows, int64_t tokens, const int64_t* slots,
                             const bnb4_kv_cache& c, int num_sms, cudaStream_t s) {
   const KvArgs a = args_of(rows, tokens, slots, c);
-  const dim3 grid(grid_for(a, c.head_dim, num_sms)), block(kThreads);
-  const bool prog = programmatic_after_kernel(s);
+  const dim3 grid(grid_for(a, num_sms)), block(kThreads);
+  const bool prog = programmatic_after_kernel(s), nf4 = c.qtype == kQtNF4;
 #define BNB4_WRITE(DV, BSV)                                                                    \
   return c.dtype == BNB4_F16                                                                   \
-             ? launch_kernel(kv_write_kernel<DV, BSV, BNB4_F16>, grid, block, 0, s, prog, a)   \
-             : launch_kernel(kv_write_kernel<DV, BSV, BNB4_BF16>, grid, block, 0, s, prog, a);
+             ? launch_kernel(nf4 ? kv_write_kernel<DV, BSV, BNB4_F16, kQtNF4>                  \
+                                 : kv_write_kernel<DV, BSV, BNB4_F16, kQtFP4>,                 \
+                             grid, block, 0, s, prog, a)                                       \
+             : launch_kernel(nf4 ? kv_write_kernel<DV, BSV, BNB4_BF16, kQtNF4>                 \
+                                 : kv_write_kernel<DV, BSV, BNB4_BF16, kQtFP4>,                \
+                             grid, block, 0, s, prog, a);
   BNB4_KV_SHAPES(BNB4_WRITE)
 #undef BNB4_WRITE
 }
@@ -334,7 +353,7 @@ cudaError_t launch_kv_write(const KvRows& rows, int64_t tokens, const int64_t* s
 cudaError_t launch_kv_read(const bnb4_kv_cache& c, const int64_t* slots, int64_t tokens,
                            const KvRows& rows, int out_dtype, int num_sms, cudaStream_t s) {
   const KvArgs a = args_of(rows, tokens, slots, c);
-  const dim3 grid(grid_for(a, c.head_dim, num_sms)), block(kThreads);
+  const dim3 grid(grid_for(a, num_sms)), block(kThreads);
   const bool prog = programmatic_after_kernel(s);
 #define BNB4_READ_T(DV, BSV, FV)                                                              \
   switch (out_dtype) {                                                                        \

@@ -84,7 +84,7 @@ def attn(**kw):
     d = dict(q=A, q_stride_t=1024, q_stride_h=128, out=A, out_stride_t=1024, out_stride_h=128,
              lse=None, cache=cache(), block_table=A, block_table_stride=8, seq_lens=A,
              cu_seqlens_q=None, workspace=A, workspace_bytes=1 << 30, total_q=3, batch=3,
-             n_heads=8, max_q_len=1, max_seq_len=100, block_table_width=8, causal=1, window=0,
+             n_heads=8, max_q_len=1, max_seq_len=100000, block_table_width=8, causal=1, window=0,
              scale=0.1, reserved=0)
     d.update(kw)
     a = bnb4.Attn()
