@@ -96,8 +96,8 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t lane_base) {
 
 // KR: the second 128 bytes of an entry hold what the first rounded away.
 template <bool KR>
-__device__ __forceinline__ void build_table(int qtype, int warps) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void build_table(int qtype, int warp, int warps) {
+  const int lane = threadIdx.x & 31;
   const int c = lane & 15;
   const float v = qtype == kQtNF4 ? __fmul_rn(nf4_value(c), kNf4Scale)
                                   : rintf(__fmul_rn(code_value(kQtFP4, c), 12.0f)) * 0.5f;
@@ -146,6 +146,12 @@ struct Scales {
       asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
     }
   }
+  // finite2: the largest finite pattern in both halves
+  __device__ __forceinline__ bool not_finite(uint32_t finite2) const {
+    uint32_t x = w[0];
+    if constexpr (NB == 4) x = __vmaxu2(x, w[1]);
+    return __vmaxu2(x, finite2) != finite2;
+  }
   template <int F>
   __device__ __forceinline__ float at(int b) const {
     const uint32_t x = w[b / 2];
@@ -176,7 +182,7 @@ template <int D, int BS, int F, int NT, bool KR>
 struct Shape {
   static constexpr int NS = NT == 1 ? 4 : 2;           // 16-token sub-tiles per tile
   static constexpr int ST = NT == 1 ? 1 : 2;           // tiles in flight per warp
-  static constexpr int W = NT == 1 && !KR ? 16 : 12;   // warps
+  static constexpr int W = 12;                         // warps
   static constexpr int GW = W / 2;                     // warps per group
   static constexpr int RT = 8 * NT, TILE = 16 * NS, NB = D / BS, KS = D / 16;
   static constexpr int kCodes = TILE * D / 2, kScales = TILE * NB * 2;
@@ -218,6 +224,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
   constexpr int NB = S::NB, KS = S::KS;
   constexpr int SW = BS / 8;  // values of a block per strip
   constexpr bool kSplitP = F == BNB4_F16;
+  constexpr uint32_t kInf = F == BNB4_BF16 ? 0x7f80u : 0x7c00u;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[W][2 * ST];
   __shared__ Ctl ctl;
@@ -246,7 +253,8 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
     ctl.wait_limit_ns = kWaitLimitNs;
     ctl.abort = 0;
   }
-  build_table<KR>(a.qtype, W);
+  // the table is built by the warps that do not look for their group's run below
+  if (gw != 0) build_table<KR>(a.qtype, warp - 1 - grp, W - 2);
   pdl_wait();
 
   // -------- this group's run of the line of tiles, or its items in turn
@@ -296,104 +304,105 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
     }
   }
   __syncthreads();
-  int b = 0, h = 0, tile0 = 0, left = 1;
-  int64_t item = run;
-  const int64_t items = static_cast<int64_t>(a.batch) * a.heads;
-  if (a.split) {
-    b = sm_item[grp][0], h = sm_item[grp][1], tile0 = sm_item[grp][2];
-    left = sm_item[grp][3];
-  }
-
   // this warp's tiles: ST of keys, then ST of values
   const uint32_t my_k = S::tiles(warp);
   const uint32_t my_v = my_k + ST * S::kStage;
+  // a lane's copies: where in a stage, how many bytes, from which array
+  const int copy_u = lane >> 1;
+  const uint32_t copy_at =
+      lane & 1 ? S::kCodes + copy_u * (S::kScales / NS) : copy_u * (S::kCodes / NS);
+  const uint32_t copy_bytes = lane & 1 ? S::kScales / NS : S::kCodes / NS;
+  const int copy_row = lane & 1 ? 2 * NB : D / 2;
+  const uint8_t* copy_k = lane & 1 ? reinterpret_cast<const uint8_t*>(a.k_absmax) : a.k_codes;
+  const uint8_t* copy_v = lane & 1 ? reinterpret_cast<const uint8_t*>(a.v_absmax) : a.v_codes;
   uint32_t put = 0, got = 0;  // tiles issued and consumed; slot = count % ST
   bool ok_all = true;         // no wait gave up
 
-  for (;;) {
+  // The group's segments: the pair (b, h) and its tiles tile0 .. tile1 - 1.
+  struct Seg {
+    int b, h, tile0, tile1;
+    Span sp;
+  };
+  int left = a.split ? sm_item[grp][3] : 0;  // tiles left of the run
+  int64_t item = run;
+  const int64_t items = static_cast<int64_t>(a.batch) * a.heads;
+  // the next segment from (b, h, tile0) on; false: there is none
+  auto find = [&](Seg& g2) {
     if (a.split) {
-      if (left <= 0 || b >= a.batch) break;
+      while (left > 0 && g2.b < a.batch) {
+        g2.sp = span_of<RT, TILE>(a, g2.b, 0);
+        if (g2.sp.rows > 0) {
+          g2.tile1 = g2.sp.tiles - g2.tile0 <= left ? g2.sp.tiles : g2.tile0 + left;
+          left -= g2.tile1 - g2.tile0;
+          return true;
+        }
+        ++g2.b, g2.h = 0, g2.tile0 = 0;  // holds no tiles
+      }
     } else {
-      if (item >= items) break;
-      h = static_cast<int>(item % a.heads);
-      b = static_cast<int>(item / a.heads);
-      item += runs;
-    }
-    const Span sp = span_of<RT, TILE>(a, b, 0);
-    if (sp.rows == 0) {  // uniform over the group
-      if (a.split) ++b, h = 0, tile0 = 0;  // holds no tiles
-      continue;
-    }
-    const int tile1 = !a.split || sp.tiles - tile0 <= left ? sp.tiles : tile0 + left;
-    const int32_t* bt = a.block_table + static_cast<int64_t>(b) * a.bt_stride;
-
-    // page of sub-tile `lane` of tile i; -1: no token of it is cached
-    auto page_of = [&](int i) {
-      int pg = -1;
-      if (lane < NS && i < tile1) {
-        const int j = sp.base + i * TILE + 16 * lane;
-        if (j < sp.end) {
-          const int p = __ldg(bt + a.page.div(static_cast<uint32_t>(j)));
-          if (p >= 0 && p < a.num_pages) pg = p;
+      for (; item < items; item += runs) {
+        g2.h = static_cast<int>(item % a.heads);
+        g2.b = static_cast<int>(item / a.heads);
+        g2.sp = span_of<RT, TILE>(a, g2.b, 0);
+        if (g2.sp.rows > 0) {
+          g2.tile0 = 0, g2.tile1 = g2.sp.tiles;
+          item += runs;
+          return true;
         }
       }
-      return pg;
-    };
-    // copies of tile i's keys (or values) into the slot `n % ST`: lanes 2 s
-    // and 2 s + 1 bring sub-tile s's codes and scales
-    auto issue = [&](int i, int pages, uint32_t n, bool values) {
-      const uint32_t at = (values ? my_v : my_k) + (n % ST) * S::kStage;
-      const uint32_t bar = smem_u32(&bars[warp][(values ? ST : 0) + n % ST]);
-      const unsigned have = __ballot_sync(0xffffffffu, pages >= 0);
-      if (lane == 0)
-        mbar_arrive_expect_tx(bar, __popc(have) * (S::kCodes / NS + S::kScales / NS));
-      const int s = lane >> 1;
-      const int pg = __shfl_sync(0xffffffffu, pages, s);  // orders the reads before, too
-      if (s < NS && pg >= 0) {
-        const uint32_t j = static_cast<uint32_t>(sp.base + i * TILE + 16 * s);
-        const uint32_t in = j - a.page.div(j) * a.page.d;
-        const int64_t row = (static_cast<int64_t>(pg) * a.heads + h) * a.page.d + in;
-        if (lane & 1)
-          copy_to_shared(at + S::kCodes + s * (S::kScales / NS),
-                         (values ? a.v_absmax : a.k_absmax) + row * NB, S::kScales / NS, bar);
-        else
-          copy_to_shared(at + s * (S::kCodes / NS), (values ? a.v_codes : a.k_codes) + row * (D / 2),
-                         S::kCodes / NS, bar);
-      }
-      return have;
-    };
-    auto wait = [&](uint32_t n, bool values) {
-      const uint32_t bar = smem_u32(&bars[warp][(values ? ST : 0) + n % ST]);
-      if (!wait_bounded(bar, (n / ST) & 1, &ctl, a.err)) ok_all = false;
-      __syncwarp();
-    };
-
-    // the first tiles are on their way while q is read
-    unsigned have = 0;  // sub-tiles present, NS bits per tile in flight, oldest lowest
-#pragma unroll
-    for (int x = 0; x < ST; ++x) {
-      const int i = tile0 + gw + x * GW;
-      if (i < tile1 && ok_all) {  // after a failed wait nothing more is issued, but
-        const int pages = page_of(i);  // the group's barriers below are still met
-        have |= issue(i, pages, put, false) << (NS * x);
-        issue(i, pages, put, true);
-        ++put;
-      }
     }
-    int pages_next = page_of(tile0 + gw + ST * GW);
+    return false;
+  };
 
-    // ---------------- q: rows g (and g + 8) as the B operand of every k-step
-    uint32_t qf[NT][KS][2];
-    float qs[NT][2];  // per column 2 t, 2 t + 1: score in log2 units = sum of products * qs
+  // A tile's copies: lane 2 u brings sub-tile u's codes, lane 2 u + 1 its
+  // scales.  The page entry of the lane's sub-tile of tile i (-1: no cached
+  // token) is read a tile ahead of its use.
+  auto page_of = [&](const Seg& w, int i) {
+    const int j = w.sp.base + i * TILE + 16 * (lane >> 1);
+    return lane < 2 * NS && i < w.tile1 && j < w.sp.end
+               ? __ldg(a.block_table + static_cast<int64_t>(w.b) * a.bt_stride +
+                       a.page.div(static_cast<uint32_t>(j)))
+               : -1;
+  };
+  auto row_of = [&](const Seg& w, int i, int entry) {  // the sub-tile's first cache row, or -1
+    const uint32_t j = static_cast<uint32_t>(w.sp.base + i * TILE + 16 * (lane >> 1));
+    const uint32_t in = j - a.page.div(j) * a.page.d;
+    return entry >= 0 && entry < a.num_pages
+               ? (static_cast<int64_t>(entry) * a.heads + w.h) * a.page.d + in
+               : static_cast<int64_t>(-1);
+  };
+  // into slot n % ST; returns bit 2 u for each sub-tile u that is there
+  auto issue = [&](int64_t row, uint32_t n, bool values) {
+    const uint32_t at = (values ? my_v : my_k) + (n % ST) * S::kStage + copy_at;
+    const uint32_t bar = smem_u32(&bars[warp][(values ? ST : 0) + n % ST]);
+    const unsigned have = __ballot_sync(0xffffffffu, row >= 0) & 0x55555555u;
+    if (lane == 0)
+      mbar_arrive_expect_tx(bar, __popc(have) * (S::kCodes / NS + S::kScales / NS));
+    __syncwarp();  // also orders the slot's last reads before the copies
+    if (row >= 0)
+      copy_to_shared(at, (values ? copy_v : copy_k) + row * copy_row, copy_bytes, bar);
+    return have;
+  };
+  auto wait = [&](uint32_t n, bool values) {
+    const uint32_t bar = smem_u32(&bars[warp][(values ? ST : 0) + n % ST]);
+    if (!wait_bounded(bar, (n / ST) & 1, &ctl, a.err)) ok_all = false;
+    __syncwarp();
+  };
+
+  // Starts a segment: its first tiles are on their way, and its rows of q (as B
+  // operand of every k-step: rows g and g + 8) are being read -- with 16 rows
+  // only later, for want of registers while the segment before is joined.
+  constexpr uint32_t kAll = 0x55u & ((1u << 2 * NS) - 1);
+  unsigned have = 0;  // sub-tiles present, 2 NS bits per tile in flight, oldest lowest
+  int entry_next = -1;
+  uint32_t raw[NT][KS][2];
+  auto read_q = [&](const Seg& w) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = sp.r0 + 8 * n + g;
-      const bool real = 8 * n + g < sp.rows;
+      const bool real = 8 * n + g < w.sp.rows;
+      const int r = real ? w.sp.r0 + 8 * n + g : 0;
       const int i = r / a.group, hh = r - i * a.group;
-      const uint16_t* src = a.q + (static_cast<int64_t>(sp.q0) + i) * a.q_ts +
-                            (static_cast<int64_t>(h) * a.group + hh) * a.q_hs;
-      uint32_t raw[KS][2];
-      uint32_t top = 0;
+      const uint16_t* src = a.q + (static_cast<int64_t>(w.sp.q0) + i) * a.q_ts +
+                            (static_cast<int64_t>(w.h) * a.group + hh) * a.q_hs;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -402,13 +411,49 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
           const int p = t * (D / 4) + 4 * s + 2 * e;
           const int strip = p / (D / 8), x = p % (D / 8);
           const int d = (x / SW) * BS + strip * SW + x % SW;
-          raw[s][e] = real ? __ldg(reinterpret_cast<const uint32_t*>(src + d)) : 0u;
+          raw[n][s][e] = real ? __ldg(reinterpret_cast<const uint32_t*>(src + d)) : 0u;
         }
+    }
+  };
+  auto start = [&](const Seg& w) {
+    int entry[ST + 1];
+#pragma unroll
+    for (int x = 0; x < ST + 1; ++x) entry[x] = page_of(w, w.tile0 + gw + x * GW);
+    if constexpr (NT == 1) read_q(w);
+    have = 0;
+#pragma unroll
+    for (int x = 0; x < ST; ++x) {
+      const int i = w.tile0 + gw + x * GW;
+      if (i < w.tile1 && ok_all) {  // after a failed wait nothing more is issued, but
+                                    // the group's barriers below are still met
+        const int64_t row = row_of(w, i, entry[x]);
+        have |= issue(row, put, false) << (2 * NS * x);
+        issue(row, put, true);
+        ++put;
+      }
+    }
+    entry_next = entry[ST];
+  };
+
+  Seg cur;
+  cur.b = cur.h = cur.tile0 = 0;
+  if (a.split) cur.b = sm_item[grp][0], cur.h = sm_item[grp][1], cur.tile0 = sm_item[grp][2];
+  bool more_segs = find(cur);
+  if (more_segs) start(cur);
+  while (more_segs) {  // uniform over the group
+    const Span sp = cur.sp;
+    const int h = cur.h, tile0 = cur.tile0, tile1 = cur.tile1;
+    if constexpr (NT > 1) read_q(cur);
+    uint32_t qf[NT][KS][2];
+    float qs[NT][2];  // per column 2 t, 2 t + 1: score in log2 units = sum of products * qs
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t top = 0;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          top = max(top, max(raw[s][e] & 0x7fffu, (raw[s][e] >> 16) & 0x7fffu));
+          top = max(top, max(raw[n][s][e] & 0x7fffu, (raw[n][s][e] >> 16) & 0x7fffu));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       float mul = a.scale_log2;
@@ -421,10 +466,10 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            qf[n][s][x] = pack_f16x2(bf16_lo(raw[s][x]) * f, bf16_hi(raw[s][x]) * f);
+            qf[n][s][x] = pack_f16x2(bf16_lo(raw[n][s][x]) * f, bf16_hi(raw[n][s][x]) * f);
       } else {
 #pragma unroll
-        for (int s = 0; s < KS; ++s) qf[n][s][0] = raw[s][0], qf[n][s][1] = raw[s][1];
+        for (int s = 0; s < KS; ++s) qf[n][s][0] = raw[n][s][0], qf[n][s][1] = raw[n][s][1];
       }
       // a row with an infinite or NaN entry is NaN, whatever its products are
       if (top >= (F == BNB4_BF16 ? 0x7f80u : 0x7c00u)) mul = __int_as_float(0x7fffffff);
@@ -460,12 +505,13 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
     const int tok_g = g ^ ((g >> 1) & 1);
 
     for (int i = tile0 + gw; i < tile1 && ok_all; i += GW) {
-      const uint32_t ok = have & ((1u << NS) - 1);
-      have >>= NS;
+      const uint32_t ok = have & kAll;
+      have >>= 2 * NS;
       const uint32_t kb = my_k + (got % ST) * S::kStage, vb = my_v + (got % ST) * S::kStage;
       wait(got, false);
       // ------------------------------------------------ scores
       float s[NS][NT][4];
+      uint32_t kmax = 0;  // largest patterns of the key scales, in both halves
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         Chunk<D / 8> k0, k1;
@@ -474,6 +520,8 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
         Scales<NB> s0, s1;
         s0.load(kb + S::kCodes + (16 * u + tok_g) * (2 * NB));
         s1.load(kb + S::kCodes + (16 * u + tok_g + 8) * (2 * NB));
+#pragma unroll
+        for (int y = 0; y < (NB + 1) / 2; ++y) kmax = __vmaxu2(kmax, __vmaxu2(s0.w[y], s1.w[y]));
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
           float acc[NT][4];
@@ -509,11 +557,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
             }
             first = false;
           }
-          // an infinite scale would make every product infinite or NaN; its
-          // row's score is NaN
-          float f0 = s0.template at<F>(blk), f1 = s1.template at<F>(blk);
-          f0 += f0 - f0;
-          f1 += f1 - f1;
+          const float f0 = s0.template at<F>(blk), f1 = s1.template at<F>(blk);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             s[u][n][0] = blk ? fmaf(acc[n][0], f0, s[u][n][0]) : acc[n][0] * f0;
@@ -523,14 +567,35 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
           }
         }
       }
+      // an infinite scale makes every product infinite or NaN: a token with a
+      // scale that is not finite has a NaN score
+      constexpr uint32_t kFinite2 = (kInf - 1) * 0x10001u;
+      if (__any_sync(0xffffffffu, __vmaxu2(kmax, kFinite2) != kFinite2)) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            Scales<NB> sc;
+            sc.load(kb + S::kCodes + (16 * u + tok_g + 8 * x) * (2 * NB));
+            if (sc.not_finite(kFinite2))
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                s[u][n][2 * x] = s[u][n][2 * x + 1] = __int_as_float(0x7fffffff);
+          }
+      }
       // the next tile's keys are on their way while this one's weights form
       const bool more = i + ST * GW < tile1;
-      if (more) have |= issue(i + ST * GW, pages_next, put, false) << (NS * (ST - 1));
+      int64_t row_next = -1;
+      if (more) {
+        row_next = row_of(cur, i + ST * GW, entry_next);
+        have |= issue(row_next, put, false) << (2 * NS * (ST - 1));
+      }
+      entry_next = page_of(cur, i + (ST + 1) * GW);
 
       const int j0 = sp.base + i * TILE;
-      const bool masked =
-          ok != (1u << NS) - 1 || j0 < all_lo || j0 + TILE - 1 > all_hi;  // warp-uniform
+      const bool masked = ok != kAll || j0 < all_lo || j0 + TILE - 1 > all_hi;  // warp-uniform
       if (masked) {
+        asm volatile("" ::: "memory");  // a branch, not selects on every tile
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -545,7 +610,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const int j = j0 + 16 * u + tok_g + 8 * x;
-                if (!((ok >> u) & 1u) || j > hi || j < lo) s[u][n][c + 2 * x] = -INFINITY;
+                if (!((ok >> (2 * u)) & 1u) || j > hi || j < lo) s[u][n][c + 2 * x] = -INFINITY;
               }
           }
       }
@@ -563,35 +628,62 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
         }
       wait(got, true);
       Scales<NB> vs[NS][2];
+      uint32_t vmax[(NB + 1) / 2] = {};
 #pragma unroll
       for (int u = 0; u < NS; ++u)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          vs[u][x].load(vb + S::kCodes + (16 * u + tok_g + 8 * x) * (2 * NB));
-          if (masked) {  // scales of tokens that no row sees may be anything
-            const int j = j0 + 16 * u + tok_g + 8 * x;
-            if (!((ok >> u) & 1u) || j >= sp.end || j < sp.lo)
-#pragma unroll
-              for (int y = 0; y < (NB + 1) / 2; ++y) vs[u][x].w[y] = 0u;
-          }
-        }
-      // running exponents of the value scales, and the factor that brings a
-      // weight times its scale to at most 2^15 (infinite scales stay infinite)
-      float vn[NB], vgrow[NB];
-      bool up = false;
-      constexpr uint32_t kInf = F == BNB4_BF16 ? 0x7f80u : 0x7c00u;
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
-        uint32_t x = 0;
+        for (int x = 0; x < 2; ++x) vs[u][x].load(vb + S::kCodes + (16 * u + tok_g + 8 * x) * (2 * NB));
+      if (masked) {  // scales of tokens that no row sees may be anything
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int u = 0; u < NS; ++u)
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t w = vs[u][y].w[blk / 2];
-            const uint32_t bits = (blk & 1) ? w >> 16 : w & 0xffffu;
-            x = max(x, bits < kInf ? bits : 0u);
+          for (int x = 0; x < 2; ++x) {
+            const int j = j0 + 16 * u + tok_g + 8 * x;
+            if (!((ok >> (2 * u)) & 1u) || j >= sp.end || j < sp.lo)
+#pragma unroll
+              for (int y = 0; y < (NB + 1) / 2; ++y) vs[u][x].w[y] = 0u;
           }
-        x = __reduce_max_sync(0xffffffffu, x);
+      }
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int y = 0; y < (NB + 1) / 2; ++y)
+          vmax[y] = __vmaxu2(vmax[y], __vmaxu2(vs[u][0].w[y], vs[u][1].w[y]));
+      {
+        uint32_t x = vmax[0];
+        if constexpr (NB == 4) x = __vmaxu2(x, vmax[1]);
+        if (__any_sync(0xffffffffu, __vmaxu2(x, kFinite2) != kFinite2)) {
+          // a value with a scale that is not finite makes the rows that see its
+          // token NaN, and counts as zero for the others
+#pragma unroll
+          for (int y = 0; y < (NB + 1) / 2; ++y) vmax[y] = 0;
+#pragma unroll
+          for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              if (vs[u][y].not_finite(kFinite2)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+                    if (s[u][n][2 * y + c] != -INFINITY) l[n][c] = __int_as_float(0x7fffffff);
+#pragma unroll
+                for (int z = 0; z < (NB + 1) / 2; ++z) vs[u][y].w[z] = 0u;
+              }
+#pragma unroll
+              for (int z = 0; z < (NB + 1) / 2; ++z) vmax[z] = __vmaxu2(vmax[z], vs[u][y].w[z]);
+            }
+        }
+      }
+      // running exponents of the value scales, and the factor that brings a
+      // weight times its scale to at most 2^15
+      float vn[NB], vgrow[NB];
+      bool up = false;
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        const uint32_t w = vmax[blk / 2];
+        const uint32_t x = __reduce_max_sync(0xffffffffu, (blk & 1) ? w >> 16 : w & 0xffffu);
         const int e =
             F == BNB4_BF16 ? static_cast<int>(x >> 7) - 127 : static_cast<int>(x >> 10) - 15;
         vgrow[blk] = 1.0f;
@@ -650,11 +742,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const float av = vs[u][x].template at<F>(blk) * vn[blk];
-              float y0 = p[2 * x] * av, y1 = p[2 * x + 1] * av;
-              if (masked) {  // 0 * infinity of a token that another row sees
-                y0 = s[u][n][2 * x] == -INFINITY ? 0.0f : y0;
-                y1 = s[u][n][2 * x + 1] == -INFINITY ? 0.0f : y1;
-              }
+              const float y0 = p[2 * x] * av, y1 = p[2 * x + 1] * av;
               const uint32_t hi = pack_f16x2(y0, y1);
               pb[blk][n][x] = transpose8x8(hi);
               if constexpr (kSplitP)
@@ -692,12 +780,19 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
       }
       ++got;
       if (more) {
-        issue(i + ST * GW, pages_next, put, true);
+        issue(row_next, put, true);
         ++put;
       }
-      pages_next = page_of(i + (ST + 1) * GW);
     }
     // ---------------------------------------------------- join the warps
+    // the next segment's first tiles are on their way meanwhile
+    if (a.split) {
+      cur.tile0 = 0;
+      if (++cur.h == a.heads) cur.h = 0, ++cur.b;
+    }
+    more_segs = find(cur);
+    if (more_segs) start(cur);
+
     const int busy = tile1 - tile0 < GW ? tile1 - tile0 : GW;  // warps with a tile
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -736,79 +831,74 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
           o[x][n][c + 2] = o[x][n][c + 2] * f * back;
         }
       }
-    // the upper ones of the warps that still hold sums hand them over, until warp 0 has them all: a fixed order
-    int live = busy;
-    while (live > 1) {
-      const int give = live / 2 < S::kGive ? live / 2 : S::kGive;
-      const int keep = live - give;  // warps keep .. live - 1 give to 0 ..
-      if (gw >= keep && gw < live) {
+    // The warps behind the first H hand their sums over to those (H at a time),
+    // these put theirs down, and all warps add them up, a share of the values
+    // each: a fixed order.
+    constexpr int H = S::kGive;
+    auto put_down = [&](int slot) {
+#pragma unroll
+      for (int x = 0; x < KS; ++x)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                             S::piece(grp, (slot * KS + x) * NT * 4 + n * 4 + c) + 4u * lane),
+                         "f"(o[x][n][c])
+                         : "memory");
+    };
+    auto piece_at = [&](int slot, int x, int n, int c) {
+      float y;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(y)
+                   : "r"(S::piece(grp, (slot * KS + x) * NT * 4 + n * 4 + c) + 4u * lane));
+      return y;
+    };
+#pragma unroll 1
+    for (int first = H; first < busy; first += H) {
+      if (first > H) group_sync(grp, GW * 32);  // the slots have been read
+      if (gw >= first && gw < first + H && gw < busy) put_down(gw - first);
+      group_sync(grp, GW * 32);
+      if (gw < H && first + gw < busy) {
 #pragma unroll
         for (int x = 0; x < KS; ++x)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(
-                               S::piece(grp, ((gw - keep) * KS + x) * NT * 4 + n * 4 + c) + 4u * lane),
-                           "f"(o[x][n][c])
-                           : "memory");
+            for (int c = 0; c < 4; ++c) o[x][n][c] += piece_at(gw, x, n, c);
       }
-      group_sync(grp, GW * 32);
-      if (gw < give) {
-#pragma unroll
-        for (int x = 0; x < KS; ++x)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float y;
-              asm volatile("ld.shared.f32 %0, [%1];"
-                           : "=f"(y)
-                           : "r"(S::piece(grp, (gw * KS + x) * NT * 4 + n * 4 + c) + 4u * lane));
-              o[x][n][c] += y;
-            }
-      }
-      group_sync(grp, GW * 32);
-      live = keep;
     }
+    if (gw < H && gw < busy) put_down(gw);  // its own slot, which it read last
+    group_sync(grp, GW * 32);
     const bool whole = tile0 == 0 && tile1 == sp.tiles;
-    if (gw == 0) {
-      __syncwarp();
-      // partial results: slot 0 continues the run before, slot 1 goes on in the next
-      float* part = a.ws + (static_cast<int64_t>(run) * 2 + (tile0 == 0 ? 1 : 0)) *
-                               (RT * D + 2 * RT);
+    // partial results: slot 0 continues the run before, slot 1 goes on in the next
+    float* part = a.ws + (static_cast<int64_t>(run) * 2 + (tile0 == 0 ? 1 : 0)) *
+                             (RT * D + 2 * RT);
+    const int slots = busy < H ? busy : H;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = 8 * n + 2 * t + c;
-          if (r < sp.rows) {
-            const float top = sm_max[grp][r], sum = sm_sum[grp][r];
-            if (whole) {
-              // SW values of each block, two at a time
-              const RowOut<F> out(a, sp, h, sp.r0 + r, top, sum, g == 0);
-#pragma unroll
-              for (int x = 0; x < KS; ++x)
-                out.pair((2 * x / SW) * BS + g * SW + (2 * x) % SW, o[x][n][c], o[x][n][c + 2]);
-            } else {
-#pragma unroll
-              for (int x = 0; x < KS; ++x)
-                *reinterpret_cast<float2*>(part + r * D + (2 * x / SW) * BS + g * SW +
-                                           (2 * x) % SW) = make_float2(o[x][n][c], o[x][n][c + 2]);
-              if (g == 0) {
-                part[RT * D + r] = top;
-                part[RT * D + RT + r] = sum;
-              }
-            }
+      for (int c = 0; c < 2; ++c) {
+        const int r = 8 * n + 2 * t + c;
+        if (r < sp.rows) {
+          const float top = sm_max[grp][r], sum = sm_sum[grp][r];
+          const RowOut<F> out(a, sp, h, sp.r0 + r, top, sum, whole && gw == 0 && g == 0);
+          if (!whole && gw == 0 && g == 0) {
+            part[RT * D + r] = top;
+            part[RT * D + RT + r] = sum;
+          }
+          for (int x = gw; x < KS; x += GW) {
+            float y0 = piece_at(0, x, n, c), y1 = piece_at(0, x, n, c + 2);
+            for (int w = 1; w < slots; ++w) y0 += piece_at(w, x, n, c), y1 += piece_at(w, x, n, c + 2);
+            const int d = (2 * x / SW) * BS + g * SW + (2 * x) % SW;  // two values of a block
+            if (whole)
+              out.pair(d, y0, y1);
+            else
+              *reinterpret_cast<float2*>(part + r * D + d) = make_float2(y0, y1);
           }
         }
-    }
+      }
     group_sync(grp, GW * 32);  // the shared arrays are free for the next segment
-    if (a.split) {
-      left -= tile1 - tile0;
-      tile0 = 0;
-      if (++h == a.heads) h = 0, ++b;
-    }
   }
   // a wait that gave up: copies in flight land before the CTA ends
   if (!ok_all)
