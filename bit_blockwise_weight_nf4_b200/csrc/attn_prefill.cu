@@ -35,11 +35,14 @@
 // scaling by the tile's largest scale's power of two -- an absolute error in
 // the scores --, values by a running power of two, to at most 2^16, and weights
 // by 2^7 (so at most 2^15): both stay normal 21 binades and more below the
-// largest.  Every mbarrier wait is bounded; no TMA load is used.
+// largest.  For fp16 caches, whose outputs' last place is finer than those
+// roundings, keys and values are kept in two fp16 terms (twice the products).
+// Every mbarrier wait is bounded; no TMA load is used.
 #include "attn.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "kvcache.h"
+#include "lut.cuh"
 #include "sm100.cuh"
 
 namespace bnb4 {
@@ -51,7 +54,7 @@ constexpr int TR = 128;        // rows per row tile (threads of a softmax group)
 constexpr int kRowsCta = 2 * TR;
 constexpr int kKeyWarp = 8, kValueWarp = 12, kIssueWarp = 16;
 constexpr int kThreads = 18 * 32;
-constexpr int kStages = 2;     // decoded tiles of keys, and of values
+constexpr int kMaxStages = 2;
 constexpr int kRing = 4;       // tiles' scalars: see Meta
 constexpr float kLazy = 8.0f;  // growth of the maximum that is let pass, in binades
 constexpr int kBoost = 7;      // weights are held times 2^kBoost
@@ -60,11 +63,15 @@ constexpr int kBoost = 7;      // weights are held times 2^kBoost
 __host__ __device__ constexpr int value_top(int qtype) { return qtype == kQtNF4 ? 14 : 12; }
 constexpr int kHalf = TK * 128;  // 128 rows of 128 bytes
 
-template <int D>
+// HL: keys and values are held in two fp16 terms each (fp16 caches: see the
+// precision note above), a tile of both at a time instead of two.
+template <int D, bool HL>
 struct Smem {
+  static constexpr int kStages = HL ? 1 : 2;         // decoded tiles of keys, and of values
   static constexpr int kQ = (D / 64) * kHalf;        // one row tile of q
-  static constexpr int kK = (D / 64) * kHalf;        // one tile of keys
-  static constexpr int kV = (TK / 64) * D * 128;     // one tile of values
+  static constexpr int kKTerm = (D / 64) * kHalf;    // one tile of keys, a term
+  static constexpr int kVTerm = (TK / 64) * D * 128; // one tile of values, a term
+  static constexpr int kK = kKTerm * (HL ? 2 : 1), kV = kVTerm * (HL ? 2 : 1);
   static constexpr int kOffK = 2 * kQ;
   static constexpr int kOffV = kOffK + kStages * kK;
   static constexpr int kOffTable = kOffV + kStages * kV;
@@ -85,7 +92,7 @@ struct Ctl {
   // of a row tile: q is there; a half's scores and its weights are complete;
   // the sums are, but for the last half, and in the end
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2], done[2];
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
   uint64_t m_full[kRing];
   uint64_t wait_limit_ns;
   uint32_t tmem_base;
@@ -178,6 +185,11 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_store_done() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -187,6 +199,33 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void group_sync(int id) {
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
+// What mul_f16x2(t, f) rounded away (exact in one fma, but for subnormal
+// results), and the table's own residue r times f.
+__device__ __forceinline__ uint32_t rest_f16x2(uint32_t t, uint32_t r, uint32_t f, uint32_t y) {
+  return fma_f16x2(r, f, fma_f16x2(t, f, y ^ 0x80008000u));
+}
+
+// The residues of the table's fp16 roundings, for byte permutes (lut.cuh).
+__device__ __forceinline__ Lut make_residues(int qtype) {
+  uint32_t P[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float n0 = __fmul_rn(nf4_value(2 * j), kNf4Scale);
+    const float n1 = __fmul_rn(nf4_value(2 * j + 1), kNf4Scale);
+    const uint32_t h = pack_f16x2(n0, n1);
+    P[j] = qtype == kQtNF4 ? pack_f16x2(__fsub_rn(n0, half_to_f32<BNB4_F16>(h & 0xffffu)),
+                                        __fsub_rn(n1, half_to_f32<BNB4_F16>(h >> 16)))
+                           : 0u;  // E2M1's magnitudes are exact
+  }
+  Lut l;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    l.L[q] = prmt(P[2 * q], P[2 * q + 1], 0x6420);
+    l.H[q] = prmt(P[2 * q], P[2 * q + 1], 0x7531);
+  }
+  return l;
+}
+
 // The table of code pairs: entry `byte` holds the fp16 pair {t[byte >> 4],
 // t[byte & 15]} (times the table's constant), one copy per bank.
 __device__ __forceinline__ void build_pairs(uint32_t at, int qtype, int warp, int warps) {
@@ -241,8 +280,9 @@ struct PrefillArgs {
 
 template <int D, int BS, int F>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const PrefillArgs pa) {
-  using S = Smem<D>;
-  constexpr int NB = D / BS;
+  constexpr bool HL = F == BNB4_F16;
+  using S = Smem<D, HL>;
+  constexpr int NB = D / BS, kStages = S::kStages;
   const AttnArgs& a = pa.a;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -411,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         tmem_load_done(v);
         tmem_load_done(w);
         if (masked) {
+          asm volatile("" ::: "memory");  // a branch, not selects on every tile
           mask32(v, present, lo, hi);
           mask32(w, present >> 2, lo - 32, hi - 32);
         }
@@ -547,6 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
     const bool values = warp >= kValueWarp;
     const int u = static_cast<int>(threadIdx.x) - (values ? kValueWarp : kKeyWarp) * 32;
     const uint32_t lane_table = smem_u32(smem + S::kOffTable) + 4u * lane;
+    Lut residues;
+    if constexpr (HL) residues = make_residues(a.qtype);
     // a token's page entry, read two tiles ahead (-1: not cached), and its cache
     // row, computed when the entry has arrived
     auto entry_of = [&](int tile, int tok) {
@@ -677,9 +720,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
             // word x0 + y holds stored places 8 (x0 + y) ..: of one block, or two of
             // 4 values; 4 words are whole strips, so the blocks follow from y
             const int b0 = ((8 * y) % (D / 8)) / (BS / 8), b1 = ((8 * y + 4) % (D / 8)) / (BS / 8);
-            *reinterpret_cast<uint4*>(dst + (x0 / 8) * kHalf + ((((x0 & 7) + y) ^ (u & 7)) << 4)) =
-                make_uint4(mul_f16x2(v.x, fac[b0]), mul_f16x2(v.y, fac[b0]),
-                           mul_f16x2(v.z, fac[b1]), mul_f16x2(v.w, fac[b1]));
+            const uint4 k = make_uint4(mul_f16x2(v.x, fac[b0]), mul_f16x2(v.y, fac[b0]),
+                                       mul_f16x2(v.z, fac[b1]), mul_f16x2(v.w, fac[b1]));
+            uint8_t* at = dst + (x0 / 8) * kHalf + ((((x0 & 7) + y) ^ (u & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = k;
+            if constexpr (HL) {
+              const uint4 r = dq8(residues, w[y]);
+              *reinterpret_cast<uint4*>(at + S::kKTerm) = make_uint4(
+                  rest_f16x2(v.x, r.x, fac[b0], k.x), rest_f16x2(v.y, r.y, fac[b0], k.y),
+                  rest_f16x2(v.z, r.z, fac[b1], k.z), rest_f16x2(v.w, r.w, fac[b1], k.w));
+            }
           }
 #pragma unroll
           for (int y = 0; y < 12; ++y) w[y] = w[y + 4];
@@ -702,20 +752,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           const int b0 = ((8 * word) % (D / 8)) / (BS / 8);
           uint4 g = *reinterpret_cast<const uint4*>(&value_scale[b0][8 * group]);
           uint8_t* dst = half + 8 * word * 128;
+          // row 8 word + y of the operand: the pairs of tokens t[0] .. t[3]
+          auto put_row = [&](int y, const uint32_t (&t)[4]) {
+            const uint4 v = make_uint4(
+                mul_f16x2(pair_of<0>(t[0], lane_table), g.x),
+                mul_f16x2(pair_of<0>(t[1], lane_table), g.y),
+                mul_f16x2(pair_of<0>(t[2], lane_table), g.z),
+                mul_f16x2(pair_of<0>(t[3], lane_table), g.w));
+            uint8_t* at = dst + y * 128 + (((group & 7) ^ y) << 4);
+            *reinterpret_cast<uint4*>(at) = v;
+            if constexpr (HL) {
+              // the codes of one byte each, as two of a word's eight
+              const uint4 r0 = dq8(residues, (t[0] & 0xffu) | (t[1] & 0xffu) << 8 |
+                                                 (t[2] & 0xffu) << 16 | t[3] << 24);
+              *reinterpret_cast<uint4*>(at + S::kVTerm) = make_uint4(
+                  rest_f16x2(pair_of<0>(t[0], lane_table), r0.x, g.x, v.x),
+                  rest_f16x2(pair_of<0>(t[1], lane_table), r0.y, g.y, v.y),
+                  rest_f16x2(pair_of<0>(t[2], lane_table), r0.z, g.z, v.z),
+                  rest_f16x2(pair_of<0>(t[3], lane_table), r0.w, g.w, v.w));
+            }
+          };
 #pragma unroll 1
           for (int y = 0; y < 8; y += 2) {  // values 8 word + y and the next: byte y / 2
             if (BS == 32 && y == 4)
               g = *reinterpret_cast<const uint4*>(&value_scale[b0 + 1][8 * group]);
-            *reinterpret_cast<uint4*>(dst + y * 128 + (((group & 7) ^ y) << 4)) = make_uint4(
-                mul_f16x2(pair_of<0>(ev[0], lane_table), g.x),
-                mul_f16x2(pair_of<0>(ev[1], lane_table), g.y),
-                mul_f16x2(pair_of<0>(ev[2], lane_table), g.z),
-                mul_f16x2(pair_of<0>(ev[3], lane_table), g.w));
-            *reinterpret_cast<uint4*>(dst + (y + 1) * 128 + (((group & 7) ^ (y + 1)) << 4)) =
-                make_uint4(mul_f16x2(pair_of<0>(od[0], lane_table), g.x),
-                           mul_f16x2(pair_of<0>(od[1], lane_table), g.y),
-                           mul_f16x2(pair_of<0>(od[2], lane_table), g.z),
-                           mul_f16x2(pair_of<0>(od[3], lane_table), g.w));
+            put_row(y, ev);
+            put_row(y + 1, od);
 #pragma unroll
             for (int x = 0; x < 4; ++x) ev[x] >>= 8, od[x] >>= 8;
           }
@@ -750,6 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
       for (int x = 0; x < D / 16; ++x)
         umma_ss(one, s_col(r) + TH * hf, q_lo + (x / 4) * (kHalf / 16) + 2 * (x & 3),
                 k + (x / 4) * (kHalf / 16) + 2 * (x & 3), kIdescS, x > 0);
+      if constexpr (HL) {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          umma_ss(one, s_col(r) + TH * hf, q_lo + (x / 4) * (kHalf / 16) + 2 * (x & 3),
+                  k + S::kKTerm / 16 + (x / 4) * (kHalf / 16) + 2 * (x & 3), kIdescS, 1u);
+      }
       umma_commit(one, bar(ctl->s_full[r][hf]));
       if (hf) umma_commit(one, bar(ctl->k_empty[j % kStages]));
     };
@@ -762,6 +830,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
 #pragma unroll
       for (int k = 0; k < TH / 16; ++k)
         umma_ts(one, o_col(r), s_col(r) + TH * hf + 8 * k, v + 2 * k, kIdescO, i > 0 || k > 0);
+      if constexpr (HL) {
+#pragma unroll
+        for (int k = 0; k < TH / 16; ++k)
+          umma_ts(one, o_col(r), s_col(r) + TH * hf + 8 * k, v + S::kVTerm / 16 + 2 * k, kIdescO,
+                  1u);
+      }
       if (hf) umma_commit(one, bar(ctl->v_empty[j % kStages]));
     };
     if (r < nr && T > 0) {
@@ -839,7 +913,7 @@ int splits_for(int64_t items, int64_t span, int num_sms) {
 
 template <int D, int BS, int F>
 cudaError_t launch_t(const PrefillArgs& pa, int64_t items, cudaStream_t s) {
-  constexpr int kSmem = Smem<D>::kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
+  constexpr int kSmem = Smem<D, F == BNB4_F16>::kOffCtl + static_cast<int>(sizeof(Ctl)) + 1024;
   static_assert(kSmem + (D / BS) * TK * 2 <= 232448, "shared memory budget");
   auto kern = attn_prefill_kernel<D, BS, F>;
   cudaError_t e =
