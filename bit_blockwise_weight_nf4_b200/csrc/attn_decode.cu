@@ -909,10 +909,17 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
 
 // Joins the partial results of the pairs that several runs share: CTA i takes
 // the pair that begins in run i and goes on in run i + 1.
+// A pair may be shared by all runs (few pairs, a long context), so the parts are
+// spread over the threads, and weighted first.
+constexpr int kMaxRuns = 320;  // bound of the runs, hence of the workspace
+constexpr int kJoinThreads = 1024;
+
 template <int D, int F, int NT, int TILE>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
   constexpr int RT = 8 * NT;
   __shared__ int sm_item[5];
+  __shared__ float sm_f[kMaxRuns * RT], sm_top[RT], sm_sum[RT];
+  __shared__ float4 sm_v[kJoinThreads];
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t run = blockIdx.x;
@@ -966,32 +973,58 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   const int b = sm_item[1], h = sm_item[2], last = sm_item[3];
   const Span sp = span_of<RT, TILE>(a, b, 0);
   constexpr int64_t kPart = RT * D + 2 * RT;
-  const int64_t first_part = 2 * run + 1;
-  for (int e = threadIdx.x; e < sp.rows * (D / 4); e += blockDim.x) {
-    const int r = e / (D / 4), d = (e % (D / 4)) * 4;
-    float top = a.ws[first_part * kPart + RT * D + r];
-    for (int64_t x = run + 1; x <= last; ++x)
-      top = fmaxf(top, a.ws[2 * x * kPart + RT * D + r]);
+  const int n = last - static_cast<int>(run) + 1, rows = sp.rows;
+  // part x: this run's second slot, then the first one of the runs behind it
+  auto part_at = [&](int x) { return a.ws + (2 * (run + x) + (x == 0 ? 1 : 0)) * kPart; };
+  for (int e = threadIdx.x; e < n * rows; e += kJoinThreads)
+    sm_f[e] = part_at(e / rows)[RT * D + e % rows];
+  __syncthreads();
+  const int warp = threadIdx.x >> 5;
+  if (warp < rows) {  // a row per warp: the maximum, then weights relative to it
+    float top = -INFINITY;
+    for (int x = lane; x < n; x += 32) top = fmaxf(top, sm_f[x * rows + warp]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t x = run; x <= last; ++x) {
-      const float* part = a.ws + (x == run ? first_part : 2 * x) * kPart;
-      const float f = ex2(part[RT * D + r] - ref);
-      const float4 y = *reinterpret_cast<const float4*>(part + r * D + d);
-      sum = fmaf(part[RT * D + RT + r], f, sum);
+    for (int x = lane; x < n; x += 32) {
+      const float m = sm_f[x * rows + warp], l = part_at(x)[RT * D + RT + warp];
+      const float f = ex2(m - ref);
+      sm_f[x * rows + warp] = f;
+      sum += m == -INFINITY ? l : l * f;  // a NaN sum without a maximum stays NaN
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sm_top[warp] = top, sm_sum[warp] = sum;
+  }
+  __syncthreads();
+  const int values = rows * (D / 4), groups = kJoinThreads / values;
+  const int grp = threadIdx.x / values, e = threadIdx.x - grp * values;
+  const int r = e / (D / 4), d = (e % (D / 4)) * 4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (grp < groups) {
+#pragma unroll 4
+    for (int x = grp; x < n; x += groups) {
+      const float f = sm_f[x * rows + r];
+      const float4 y = *reinterpret_cast<const float4*>(part_at(x) + r * D + d);
       v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y);
       v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
     }
-    const RowOut<F> out(a, sp, h, r, top, sum, d == 0);
+    sm_v[threadIdx.x] = v;
+  }
+  __syncthreads();
+  if (grp == 0) {
+    for (int x = 1; x < groups; ++x) {
+      const float4 y = sm_v[x * values + e];
+      v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+    }
+    const RowOut<F> out(a, sp, h, r, sm_top[r], sm_sum[r], d == 0);
     out.pair(d, v.x, v.y);
     out.pair(d + 2, v.z, v.w);
   }
 }
 
 // ------------------------------------------------------------------- host
-constexpr int kMaxRuns = 320;  // bound of the runs, hence of the workspace
-
 // Whole pairs in turn where no pair has more than a tile per warp of a group
 // (a cut would only add the join), else the line of tiles cut into equal runs.
 template <int F, int NT, bool KR>
@@ -1017,7 +1050,7 @@ cudaError_t launch_t(AttnArgs& a, int64_t span, int num_sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_kernel(kern, dim3(grid), dim3(S::W * 32), kSmem, s, programmatic_after_kernel(s), a);
   if (e != cudaSuccess || !a.split) return e;
-  return launch_kernel(attn_join_kernel<D, F, NT, S::TILE>, dim3(2 * grid), dim3(256), 0, s, true,
+  return launch_kernel(attn_join_kernel<D, F, NT, S::TILE>, dim3(2 * grid), dim3(kJoinThreads), 0, s, true,
                        a);
 }
 

@@ -880,16 +880,20 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const PrefillArg
   constexpr int64_t kPart = kRowsCta * (D + 2);
   const float* part = a.ws + static_cast<int64_t>(item) * pa.splits * kPart;
   float top = -INFINITY;
+#pragma unroll 8
   for (int s = 0; s < pa.splits; ++s) top = fmaxf(top, part[s * kPart + kRowsCta * D + 2 * row]);
   const float ref = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
   for (int s = 0; s < pa.splits; ++s) {
     const float2 ml =
         *reinterpret_cast<const float2*>(part + s * kPart + kRowsCta * D + 2 * row);
-    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // saw nothing; its sums may be unwritten
+    // a part that saw nothing may have left its sums unwritten
+    const bool none = ml.x == -INFINITY && ml.y == 0.0f;
     const float f = ex2(ml.x - ref);
-    const float4 y = *reinterpret_cast<const float4*>(part + s * kPart + row * D + x);
+    float4 y = *reinterpret_cast<const float4*>(part + s * kPart + row * D + x);
+    if (none) y = make_float4(0.f, 0.f, 0.f, 0.f);
     // a NaN sum of a part without a maximum stays NaN
     sum += ml.x == -INFINITY ? ml.y : ml.y * f;
     v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y);
