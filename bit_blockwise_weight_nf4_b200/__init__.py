@@ -457,17 +457,29 @@ def gemv_4bit_grouped(items, outs=None, _persistent=False):
 # A decoder makes these calls once per layer and step, so the checks are
 # written to cost little: each tensor's shape and strides are fetched once,
 # and what failed is only worked out when something did.
-def _on(device, call):
-    """``call(stream)`` with the device (an index) current, on its current
-    stream."""
-    torch = _torch()
+_calls = None
+
+
+def _fast():
+    """(torch, the current device's index, a device's current stream, the
+    library): looked up once."""
+    global _calls
+    if _calls is None:
+        torch = _torch()
+        _calls = (torch, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, load())
+    return _calls
+
+
+def _call(fn, device, *args):
+    """fn(*args, stream) on the device's current stream, with the device (an
+    index) current."""
+    torch, current, stream, _ = _fast()
     if device < 0:
         raise ValueError("the cache is not on a CUDA device")
-    C = torch._C
-    if C._cuda_getDevice() == device:
-        return call(C._cuda_getCurrentRawStream(device))
+    if current() == device:
+        return fn(*args, stream(device))
     with torch.cuda.device(device):
-        return call(C._cuda_getCurrentRawStream(device))
+        return fn(*args, stream(device))
 
 
 def _need(ok, what):
@@ -486,21 +498,22 @@ class KVCache4bit:
     def __init__(self, k_codes, v_codes, k_absmax, v_absmax, blocksize=64, qtype=NF4):
         torch = _torch()
         shape, dtype, index = k_codes.shape, k_absmax.dtype, k_codes.get_device()
-        _need(len(shape) == 4 and k_codes.dtype == torch.uint8,
-              "codes are uint8 [pages, kv heads, page size, D / 2]")
-        pages, heads, page, half = shape
         dt = BF16 if dtype == torch.bfloat16 else F16 if dtype == torch.float16 else None
         if dt is None:
             raise TypeError("a cache's scales are bfloat16 or float16")
-        _need(v_codes.shape == shape and v_codes.dtype == torch.uint8,
-              "k_codes and v_codes differ in shape or dtype")
-        _need(blocksize > 0 and k_absmax.shape == (pages, heads, page, 2 * half // blocksize),
-              "k_absmax is [pages, kv heads, page size, D / blocksize]")
-        _need(v_absmax.shape == k_absmax.shape and v_absmax.dtype == dtype,
-              "k_absmax and v_absmax differ in shape or dtype")
-        for t in (k_codes, v_codes, k_absmax, v_absmax):
-            _need(t.is_contiguous() and t.get_device() == index,
-                  "a cache's tensors are contiguous and on one device")
+        u8 = torch.uint8
+        if len(shape) != 4 or blocksize <= 0 or v_codes.shape != shape or \
+                k_codes.dtype != u8 or v_codes.dtype != u8 or v_absmax.dtype != dtype:
+            raise ValueError("k_codes and v_codes are uint8 [pages, kv heads, page size, D / 2], "
+                             "k_absmax and v_absmax of one dtype")
+        pages, heads, page, half = shape
+        scales = (pages, heads, page, 2 * half // blocksize)
+        if k_absmax.shape != scales or v_absmax.shape != scales:
+            raise ValueError("the scales are [pages, kv heads, page size, D / blocksize]")
+        if not (k_codes.is_contiguous() and v_codes.is_contiguous() and
+                k_absmax.is_contiguous() and v_absmax.is_contiguous() and
+                v_codes.get_device() == k_absmax.get_device() == v_absmax.get_device() == index):
+            raise ValueError("a cache's tensors are contiguous and on one device")
         self.k_codes, self.v_codes = k_codes, v_codes
         self.k_absmax, self.v_absmax = k_absmax, v_absmax
         self.num_pages, self.n_kv_heads, self.page_size = pages, heads, page
@@ -509,6 +522,7 @@ class KVCache4bit:
         self.struct = KvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_absmax.data_ptr(),
                               v_absmax.data_ptr(), pages, page, heads, 2 * half, blocksize,
                               qtype, dt, 0)
+        self.ref = ctypes.byref(self.struct)
 
     @staticmethod
     def empty(num_pages, page_size, n_kv_heads, head_dim, dtype=None, blocksize=64, qtype=NF4,
@@ -561,15 +575,16 @@ def kv_write_4bit(k, v, cache, slots):
     token and head stride that is a multiple of 8) into the cache's slots
     ``slots`` (int64 [T]; a slot outside the cache, such as -1, leaves its
     token out; slots must differ)."""
-    torch = _torch()
-    T = k.shape[0]
-    _need(k.dtype == cache.dtype and v.dtype == cache.dtype, "k and v have the cache's dtype")
+    torch, _, _, lib = _fast()
+    T, dtype = k.shape[0], cache.dtype
+    if k.dtype != dtype or v.dtype != dtype:
+        raise ValueError("k and v have the cache's dtype")
     kp, kt, kh = _kv_rows(k, cache, T, cache.n_kv_heads, "k")
     vp, vt, vh = _kv_rows(v, cache, T, cache.n_kv_heads, "v")
     sp = _index(slots, cache, torch.int64, (T,), "slots")
-    rc = _on(cache.device_index, lambda stream: bnb_kv_write_4bit(
-        kp, kt, kh, vp, vt, vh, T, sp, cache.struct, stream))
-    _check(rc, "bnb_kv_write_4bit")
+    rc = _call(lib.bnb_kv_write_4bit, cache.device_index, kp, kt, kh, vp, vt, vh, T, sp, cache.ref)
+    if rc:
+        raise Bnb4Error(rc, "bnb_kv_write_4bit")
     return cache
 
 
@@ -578,7 +593,7 @@ def kv_read_4bit(cache, slots, out_dtype=None, out=None):
     kv heads, D] of ``out_dtype`` (fp32, bf16 or fp16; default the cache's
     dtype), or into ``out`` = (k, v), either of which may be None.  Rows of a
     slot outside the cache are not written."""
-    torch = _torch()
+    torch, _, _, lib = _fast()
     T, H, D = slots.shape[0], cache.n_kv_heads, cache.head_dim
     sp = _index(slots, cache, torch.int64, (T,), "slots")
     if out is None:
@@ -598,9 +613,9 @@ def kv_read_4bit(cache, slots, out_dtype=None, out=None):
         rows += (() if v is None else _kv_rows(v, cache, T, H, "out")) or (None, 0, 0)
     if dt is None:
         raise TypeError("kv_read_4bit writes float32, bfloat16 or float16 (one of them)")
-    rc = _on(cache.device_index, lambda stream: bnb_kv_read_4bit(
-        cache.struct, sp, T, *rows, dt, stream))
-    _check(rc, "bnb_kv_read_4bit")
+    rc = _call(lib.bnb_kv_read_4bit, cache.device_index, cache.ref, sp, T, *rows, dt)
+    if rc:
+        raise Bnb4Error(rc, "bnb_kv_read_4bit")
     return k, v
 
 
@@ -616,14 +631,17 @@ def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None
     ``lse`` (fp32 [T, heads], contiguous) receives the log-sum-exp.
     ``max_seq_len`` (default: what the block table holds) is the bound by
     which the work is split."""
-    torch = _torch()
-    i32 = torch.int32
-    T, heads = q.shape[0], q.shape[1]
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _need(q.dtype == cache.dtype and out.dtype == cache.dtype, "q and out have the cache's dtype")
+    torch, _, _, lib = _fast()
+    i32, shape, dtype = torch.int32, q.shape, q.dtype
+    T, heads = shape[0], shape[1]
     qp, qt, qh = _kv_rows(q, cache, T, None, "q")
-    op, ot, oh = _kv_rows(out, cache, T, heads, "out")
+    if dtype != cache.dtype or (out is not None and out.dtype != dtype):
+        raise ValueError("q and out have the cache's dtype")
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        op, ot, oh = out.data_ptr(), heads * shape[2], shape[2]
+    else:
+        op, ot, oh = _kv_rows(out, cache, T, heads, "out")
     table, step = block_table.shape, block_table.stride()
     if len(table) != 2 or block_table.dtype != i32 or (step[1] != 1 and table[1] > 1) or \
             block_table.get_device() != cache.device_index:
@@ -645,14 +663,17 @@ def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None
     a = Attn(qp, qt, qh, op, ot, oh, lp, ctypes.pointer(cache.struct), block_table.data_ptr(),
              step[0] if B > 1 else W, lens, cu, None, 0, T, B, heads, max_q_len, max_seq_len, W,
              1 if causal else 0, window, cache.head_dim ** -0.5 if scale is None else scale, 0)
-    rc, size = bnb4_attn_workspace(a)
-    _check(rc, "bnb_attn_4bit")
-    if size:
+    ref, need = ctypes.byref(a), ctypes.c_size_t()
+    rc = lib.bnb4_attn_workspace(ref, ctypes.byref(need))
+    if rc:
+        raise Bnb4Error(rc, "bnb_attn_4bit")
+    if need.value:
         if workspace is None:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    rc = _on(cache.device_index, lambda stream: bnb_attn_4bit(a, stream))
-    _check(rc, "bnb_attn_4bit")
+    rc = _call(lib.bnb_attn_4bit, cache.device_index, ref)
+    if rc:
+        raise Bnb4Error(rc, "bnb_attn_4bit")
     return out
 
 
