@@ -185,6 +185,31 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
 __device__ __forceinline__ void tmem_store_done() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {  // drops NaN, as fmaxf
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// two fp32 values at a time
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float lo_f32(uint64_t x) {
+  return __uint_as_float(static_cast<uint32_t>(x));
+}
+__device__ __forceinline__ float hi_f32(uint64_t x) {
+  return __uint_as_float(static_cast<uint32_t>(x >> 32));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -368,51 +393,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
       const int i = real ? rr / a.group : 0, hh = real ? rr - i * a.group : 0;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       float qs = a.scale_log2;
-      {  // q, in the stored order, as fp16
-        const uint16_t* src = a.q + (static_cast<int64_t>(sp.q0) + i) * a.q_ts +
-                              (static_cast<int64_t>(h) * a.group + hh) * a.q_hs;
-        auto chunk = [&](int c) {  // stored places 8 c ..
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (real) {
-            if constexpr (BS >= 64) {
-              x = __ldg(reinterpret_cast<const uint4*>(src + value_at<D, BS>(8 * c)));
-            } else {
-              const uint2 y0 = __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c)));
-              const uint2 y1 =
-                  __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c + 4)));
-              x = make_uint4(y0.x, y0.y, y1.x, y1.y);
+      {  // q, in the stored order, as fp16: D / 8 lanes read a row
+        constexpr int kPer = 256 / D, kSteps = 32 / kPer;  // rows per step, steps per warp
+        const int64_t mine = (static_cast<int64_t>(sp.q0) + i) * a.q_ts +
+                             (static_cast<int64_t>(h) * a.group + hh) * a.q_hs;
+        const unsigned reals = __ballot_sync(0xffffffffu, real);
+        const int c = lane % (D / 8), sub = lane / (D / 8);  // stored places 8 c .. of a row
+        uint32_t top = 0;  // of this thread's own row
+        uint8_t* dst = smem + r * S::kQ + ((warp & 3) * 32) * 128 + (c / 8) * kHalf;
+#pragma unroll
+        for (int half = 0; half < kSteps; half += 8) {
+          uint4 x[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int rw = (half + y) * kPer + sub;  // of the warp's 32
+            const int64_t at = __shfl_sync(0xffffffffu, mine, rw);
+            const uint16_t* src = a.q + at;
+            x[y] = make_uint4(0, 0, 0, 0);
+            if ((reals >> rw) & 1u) {
+              if constexpr (BS >= 64) {
+                x[y] = __ldg(reinterpret_cast<const uint4*>(src + value_at<D, BS>(8 * c)));
+              } else {
+                const uint2 y0 = __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c)));
+                const uint2 y1 =
+                    __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c + 4)));
+                x[y] = make_uint4(y0.x, y0.y, y1.x, y1.y);
+              }
             }
           }
-          return x;
-        };
-        uint32_t top = 0;  // first the row's largest, then its values (from the cache)
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = chunk(c);
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, (y[e] >> 16) & 0x7fffu));
+          for (int y = 0; y < 8; ++y) {
+            const uint32_t z[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
+            uint32_t t = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t = max(t, max(z[e] & 0x7fffu, (z[e] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = D / 16; o >= 1; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+            uint4 v = x[y];
+            if constexpr (F == BNB4_BF16) {
+              int e = static_cast<int>(t >> 7) - 127;
+              const float f = pow2(14 - (e < -100 ? -100 : e));
+              v = make_uint4(pack_f16x2(bf16_lo(v.x) * f, bf16_hi(v.x) * f),
+                             pack_f16x2(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
+                             pack_f16x2(bf16_lo(v.z) * f, bf16_hi(v.z) * f),
+                             pack_f16x2(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
+            }
+            const int rw = (half + y) * kPer + sub;
+            *reinterpret_cast<uint4*>(dst + rw * 128 + (((c & 7) ^ (rw & 7)) << 4)) = v;
+            const uint32_t own = __shfl_sync(0xffffffffu, t, (lane % kPer) * (D / 8));
+            if (lane / kPer == half + y) top = own;
+          }
         }
-        float f = 1.0f;
         if constexpr (F == BNB4_BF16) {
           int e = static_cast<int>(top >> 7) - 127;
-          e = e < -100 ? -100 : e;
-          f = pow2(14 - e);
-          qs *= pow2(e - 14);
+          qs *= pow2((e < -100 ? -100 : e) - 14);
         }
         if (top >= (F == BNB4_BF16 ? 0x7f80u : 0x7c00u)) qs = __int_as_float(0x7fffffff);
         qs *= a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale;
-        uint8_t* dst = smem + r * S::kQ + (row & (TR - 1)) * 128;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 y = chunk(c);
-          if constexpr (F == BNB4_BF16)
-            y = make_uint4(pack_f16x2(bf16_lo(y.x) * f, bf16_hi(y.x) * f),
-                           pack_f16x2(bf16_lo(y.y) * f, bf16_hi(y.y) * f),
-                           pack_f16x2(bf16_lo(y.z) * f, bf16_hi(y.z) * f),
-                           pack_f16x2(bf16_lo(y.w) * f, bf16_hi(y.w) * f));
-          *reinterpret_cast<uint4*>(dst + (c / 8) * kHalf + (((c & 7) ^ (row & 7)) << 4)) = y;
-        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(ctl->q_full[r]));
@@ -455,14 +492,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           mask32(v, present, lo, hi);
           mask32(w, present >> 2, lo - 32, hi - 32);
         }
-        float t0 = fmaxf(v[0], w[0]), t1 = fmaxf(v[1], w[1]);
+        float t[4];
 #pragma unroll
-        for (int x = 2; x < 32; x += 2) {
-          t0 = fmaxf(t0, fmaxf(v[x], w[x]));
-          t1 = fmaxf(t1, fmaxf(v[x + 1], w[x + 1]));
-        }
+        for (int x = 0; x < 4; ++x) t[x] = fmaxf(v[x], w[x]);
+#pragma unroll
+        for (int x = 4; x < 32; ++x) t[x & 3] = max3(t[x & 3], v[x], w[x]);
         // q2 > 0, or NaN (which the comparisons below ignore)
-        const float top = fmaxf(t0, t1) * q2;
+        const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * q2;
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
         const bool shift = i2 > 0 && tve != ve;
         if (__any_sync(0xffffffffu, grow) || shift) {
@@ -491,23 +527,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         }
         ve = tve;
         const float ref = (m == -INFINITY ? 0.0f : m) - static_cast<float>(kBoost);
-        float l0 = 0.0f, l1 = 0.0f;
+        uint64_t sum2 = 0;  // two sums of the weights
+        const uint64_t q22 = pair_f32(q2, q2), ref2 = pair_f32(-ref, -ref);
         uint32_t p[16];
         auto weights = [&](float (&y)[32]) {
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
-            y[x] = ex2(fmaf(y[x], q2, -ref));
-            y[x + 1] = ex2(fmaf(y[x + 1], q2, -ref));
-            l0 += y[x];
-            l1 += y[x + 1];
-            p[x / 2] = pack_f16x2(y[x], y[x + 1]);
+            const uint64_t z = fma_f32x2(pair_f32(y[x], y[x + 1]), q22, ref2);
+            const float e0 = ex2(lo_f32(z)), e1 = ex2(hi_f32(z));
+            sum2 = add_f32x2(sum2, pair_f32(e0, e1));
+            p[x / 2] = pack_f16x2(e0, e1);
           }
         };
         weights(v);
         tmem_store16(at, p);
         weights(w);
         tmem_store16(at + 16, p);
-        l += l0 + l1;
+        l += lo_f32(sum2) + hi_f32(sum2);
         // a value that is not finite, of a token that this row sees
         if ((mt.bad[2 * hf] | mt.bad[2 * hf + 1]) != 0)
           for (int x = 0; x < TH; ++x)
