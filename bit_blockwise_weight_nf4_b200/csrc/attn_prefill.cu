@@ -569,30 +569,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           const float inv = back / l;
           const int64_t tok = static_cast<int64_t>(sp.q0) + i;
           const int head = h * a.group + hh;
-          uint16_t* dst = a.out + tok * a.o_ts + head * a.o_hs;
+          const int64_t mine = tok * a.o_ts + head * a.o_hs;
+          const unsigned reals = __ballot_sync(0xffffffffu, real);
           if (real && a.lse)
             a.lse[tok * (static_cast<int64_t>(a.heads) * a.group) + head] =
                 sees ? (lse_top + lg2(l)) * 0.693147180559945f : -INFINITY;
+          // rows go through the place that q had (its products are complete), to
+          // be written whole by D / 8 lanes each
+          uint8_t* stage = smem + r * S::kQ + ((warp & 3) * 32) * 128;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             tmem_load32(o_col(r) + lanes + 32 * c, v);
             tmem_load_done(v);
-            if (real) {
 #pragma unroll
-              for (int x = 0; x < 32; x += 8) {
-                uint4 w;
-                w.x = sees ? pack2<F>(v[x] * inv, v[x + 1] * inv) : 0u;
-                w.y = sees ? pack2<F>(v[x + 2] * inv, v[x + 3] * inv) : 0u;
-                w.z = sees ? pack2<F>(v[x + 4] * inv, v[x + 5] * inv) : 0u;
-                w.w = sees ? pack2<F>(v[x + 6] * inv, v[x + 7] * inv) : 0u;
-                if constexpr (BS >= 64) {
-                  *reinterpret_cast<uint4*>(dst + value_at<D, BS>(32 * c + x)) = w;
-                } else {
-                  *reinterpret_cast<uint2*>(dst + value_at<D, BS>(32 * c + x)) =
-                      make_uint2(w.x, w.y);
-                  *reinterpret_cast<uint2*>(dst + value_at<D, BS>(32 * c + x + 4)) =
-                      make_uint2(w.z, w.w);
-                }
+            for (int x = 0; x < 32; x += 8) {
+              uint4 w;
+              w.x = sees ? pack2<F>(v[x] * inv, v[x + 1] * inv) : 0u;
+              w.y = sees ? pack2<F>(v[x + 2] * inv, v[x + 3] * inv) : 0u;
+              w.z = sees ? pack2<F>(v[x + 4] * inv, v[x + 5] * inv) : 0u;
+              w.w = sees ? pack2<F>(v[x + 6] * inv, v[x + 7] * inv) : 0u;
+              const int p = 4 * c + x / 8;  // stored places 8 p ..
+              *reinterpret_cast<uint4*>(stage + (p / 8) * kHalf + lane * 128 +
+                                        (((p & 7) ^ (lane & 7)) << 4)) = w;
+            }
+          }
+          __syncwarp();
+          const int c = lane % (D / 8), sub = lane / (D / 8);
+          constexpr int kPer = 256 / D;
+#pragma unroll 4
+          for (int y = 0; y < 32 / kPer; ++y) {
+            const int rw = y * kPer + sub;  // of the warp's 32
+            const int64_t at = __shfl_sync(0xffffffffu, mine, rw);
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + (c / 8) * kHalf + rw * 128 +
+                                                            (((c & 7) ^ (rw & 7)) << 4));
+            if ((reals >> rw) & 1u) {
+              uint16_t* dst = a.out + at;
+              if constexpr (BS >= 64) {
+                *reinterpret_cast<uint4*>(dst + value_at<D, BS>(8 * c)) = w;
+              } else {
+                *reinterpret_cast<uint2*>(dst + value_at<D, BS>(8 * c)) = make_uint2(w.x, w.y);
+                *reinterpret_cast<uint2*>(dst + value_at<D, BS>(8 * c + 4)) = make_uint2(w.z, w.w);
               }
             }
           }
