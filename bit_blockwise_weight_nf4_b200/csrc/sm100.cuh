@@ -108,6 +108,26 @@ __device__ bool wait_bounded(uint32_t bar, uint32_t parity, Ctl* bars, int* err)
   }
 }
 
+// As wait_bounded, for waits of around a microsecond between the warps of a
+// CTA: a try_wait with a time hint parks the warp and takes longer to wake it
+// than the wait itself may last, so it is first asked for without one.
+template <class Ctl>
+__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, Ctl* bars, int* err) {
+  for (int i = 0; i < 256; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*reinterpret_cast<volatile int*>(&bars->abort)) return false;
+  }
+  return wait_bounded(bar, parity, bars, err);
+}
+
 // Wait for operations this CTA started (TMA loads, MMAs) to land before it
 // tears down: unlike wait_bounded it ignores the abort flag -- those
 // operations complete on their own within microseconds -- and gives up after
