@@ -258,6 +258,7 @@ __device__ __forceinline__ void build_pairs(uint32_t at, int qtype, int warp, in
   const float v = qtype == kQtNF4 ? __fmul_rn(nf4_value(c), kNf4Scale)
                                   : rintf(__fmul_rn(code_value(kQtFP4, c), 12.0f)) * 0.5f;
   const uint32_t h = pack_f16x2(v, 0.0f) & 0xffffu;
+#pragma unroll 4
   for (int e = warp; e < 256; e += warps) {
     const uint32_t x = __shfl_sync(0xffffffffu, h, e >> 4) | __shfl_sync(0xffffffffu, h, e & 15) << 16;
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128u * e + 4u * lane), "r"(x) : "memory");
@@ -318,7 +319,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
   pdl_trigger();
-  build_pairs(smem_u32(smem + S::kOffTable), a.qtype, warp, kThreads / 32);
   pdl_wait();
 
   // this CTA's rows (the tiles with the most tokens first) and tokens
@@ -366,10 +366,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  // Every warp calls this once, when its first loads are on their way: tensor
+  // memory, the barriers and the table are there from then on.
+  uint32_t tmem = 0;
+  auto ready = [&]() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
+  };
   // columns: scores (and weights over them) of row tile r at 128 r, sums at 256 + 128 r
   auto s_col = [&](int r) { return tmem + 128u * r; };
   auto o_col = [&](int r) { return tmem + 256u + 128u * r; };
@@ -384,7 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
   if (warp < kKeyWarp) {
     // ------------------------------------------------------------ softmax
     const int r = warp >> 2;
-    if (r < nr) {
+    if (r >= nr) {
+      ready();
+    } else {
       const int row = static_cast<int>(threadIdx.x);  // of the CTA's 256
       const int rr = sp.r0 + row;
       const bool real = row < sp.rows;
@@ -399,48 +406,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         const int c = lane % (D / 8), sub = lane / (D / 8);  // stored places 8 c .. of a row
         uint32_t top = 0;  // of this thread's own row
         uint8_t* dst = smem + r * S::kQ + ((warp & 3) * 32) * 128 + (c / 8) * kHalf;
+        uint4 x[kSteps];
 #pragma unroll
-        for (int half = 0; half < kSteps; half += 8) {
-          uint4 x[8];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const int rw = (half + y) * kPer + sub;  // of the warp's 32
-            const int64_t at = __shfl_sync(0xffffffffu, mine, rw);
-            const uint16_t* src = a.q + at;
-            x[y] = make_uint4(0, 0, 0, 0);
-            if ((reals >> rw) & 1u) {
-              if constexpr (BS >= 64) {
-                x[y] = __ldg(reinterpret_cast<const uint4*>(src + value_at<D, BS>(8 * c)));
-              } else {
-                const uint2 y0 = __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c)));
-                const uint2 y1 =
-                    __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c + 4)));
-                x[y] = make_uint4(y0.x, y0.y, y1.x, y1.y);
-              }
+        for (int y = 0; y < kSteps; ++y) {
+          const int rw = y * kPer + sub;  // of the warp's 32
+          const uint16_t* src = a.q + __shfl_sync(0xffffffffu, mine, rw);
+          x[y] = make_uint4(0, 0, 0, 0);
+          if ((reals >> rw) & 1u) {
+            if constexpr (BS >= 64) {
+              x[y] = __ldg(reinterpret_cast<const uint4*>(src + value_at<D, BS>(8 * c)));
+            } else {
+              const uint2 y0 = __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c)));
+              const uint2 y1 =
+                  __ldg(reinterpret_cast<const uint2*>(src + value_at<D, BS>(8 * c + 4)));
+              x[y] = make_uint4(y0.x, y0.y, y1.x, y1.y);
             }
           }
+        }
+        ready();
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const uint32_t z[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
-            uint32_t t = 0;
+        for (int y = 0; y < kSteps; ++y) {
+          // the row's largest magnitude, as the pattern of its bits
+          uint32_t t = __vmaxu2(__vmaxu2(x[y].x & 0x7fff7fffu, x[y].y & 0x7fff7fffu),
+                                __vmaxu2(x[y].z & 0x7fff7fffu, x[y].w & 0x7fff7fffu));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t = max(t, max(z[e] & 0x7fffu, (z[e] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = D / 16; o >= 1; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
-            uint4 v = x[y];
-            if constexpr (F == BNB4_BF16) {
-              int e = static_cast<int>(t >> 7) - 127;
-              const float f = pow2(14 - (e < -100 ? -100 : e));
-              v = make_uint4(pack_f16x2(bf16_lo(v.x) * f, bf16_hi(v.x) * f),
-                             pack_f16x2(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
-                             pack_f16x2(bf16_lo(v.z) * f, bf16_hi(v.z) * f),
-                             pack_f16x2(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
-            }
-            const int rw = (half + y) * kPer + sub;
-            *reinterpret_cast<uint4*>(dst + rw * 128 + (((c & 7) ^ (rw & 7)) << 4)) = v;
-            const uint32_t own = __shfl_sync(0xffffffffu, t, (lane % kPer) * (D / 8));
-            if (lane / kPer == half + y) top = own;
+          for (int o = D / 16; o >= 1; o >>= 1)
+            t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, o));
+          t = max(t & 0xffffu, t >> 16);
+          uint4 v = x[y];
+          if constexpr (F == BNB4_BF16) {
+            int e = static_cast<int>(t >> 7) - 127;
+            const float f = pow2(14 - (e < -100 ? -100 : e));
+            v = make_uint4(pack_f16x2(bf16_lo(v.x) * f, bf16_hi(v.x) * f),
+                           pack_f16x2(bf16_lo(v.y) * f, bf16_hi(v.y) * f),
+                           pack_f16x2(bf16_lo(v.z) * f, bf16_hi(v.z) * f),
+                           pack_f16x2(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
           }
+          const int rw = y * kPer + sub;
+          *reinterpret_cast<uint4*>(dst + rw * 128 + (((c & 7) ^ (rw & 7)) << 4)) = v;
+          const uint32_t own = __shfl_sync(0xffffffffu, t, (lane % kPer) * (D / 8));
+          if (lane / kPer == y) top = own;
         }
         if constexpr (F == BNB4_BF16) {
           int e = static_cast<int>(top >> 7) - 127;
@@ -463,26 +468,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
 
       float m = -INFINITY, l = 0.0f;
       int ve = 0;
+      // of the tile: a bit per 16 tokens, tokens whose value scale is not finite, ...
+      uint32_t present = 0;
+      uint2 bad = make_uint2(0, 0);
+      int tve = 0;
+      float q2 = 0.0f;
       for (int i2 = 0; i2 < 2 * T; ++i2) {
         const int j = i2 >> 1, hf = i2 & 1;
-        if (hf == 0) warp_wait(ctl->m_full[j % kRing], (j / kRing) & 1);
-        warp_wait(ctl->s_full[r][hf], j & 1);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t at = s_col(r) + lanes + TH * hf;
         const Meta& mt = ctl->meta[j % kRing];
-        // a bit per 16 tokens of the half
-        const uint32_t pr = *reinterpret_cast<const uint16_t*>(mt.present + 2 * hf);
-        const uint32_t present = (pr & 3u) | ((pr >> 6) & 12u);
-        const int tve = mt.value_exp;
-        float q2 = qs * pow2(mt.key_exp);
-        if (q2 == 0.0f) q2 = 0x1p-126f;  // so that -infinity stays masked
-        const int j0 = sp.base + (tile0 + j) * TK + TH * hf;
-        const bool masked = present != 15u || j0 < all_lo || j0 + TH - 1 > all_hi;  // warp-uniform
-        // columns lo .. hi of the half are inside what the row sees
-        const int lo = see_lo - j0, hi = see_hi - j0;
+        if (hf == 0) {
+          warp_wait(ctl->m_full[j % kRing], (j / kRing) & 1);
+          const uint32_t pr = *reinterpret_cast<const uint32_t*>(mt.present);
+          present = (pr & 3u) | ((pr >> 6) & 12u) | ((pr >> 12) & 48u) | ((pr >> 18) & 192u);
+          bad = make_uint2(mt.bad[0] | mt.bad[1], mt.bad[2] | mt.bad[3]);
+          tve = mt.value_exp;
+          q2 = qs * pow2(mt.key_exp);
+          if (q2 == 0.0f) q2 = 0x1p-126f;  // so that -infinity stays masked
+        } else {
+          present >>= 4;
+          bad.x = bad.y;
+        }
+        warp_wait(ctl->s_full[r][hf], j & 1);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         float v[32], w[32];
         tmem_load32(at, v);
         tmem_load32(at + 32, w);
+        const int j0 = sp.base + (tile0 + j) * TK + TH * hf;
+        const bool masked = (present & 15u) != 15u || j0 < all_lo || j0 + TH - 1 > all_hi;  // warp-uniform
+        // columns lo .. hi of the half are inside what the row sees
+        const int lo = see_lo - j0, hi = see_hi - j0;
         tmem_load_done(v);
         tmem_load_done(w);
         if (masked) {
@@ -492,9 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         }
         float t[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) t[x] = fmaxf(v[x], w[x]);
+        for (int x = 0; x < 4; ++x) t[x] = fmaxf(v[x], v[x + 4]);
 #pragma unroll
-        for (int x = 4; x < 32; ++x) t[x & 3] = max3(t[x & 3], v[x], w[x]);
+        for (int x = 8; x < 32; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) t[y] = max3(t[y], v[x + y], v[x + y + 4]);
+#pragma unroll
+        for (int x = 0; x < 32; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) t[y] = max3(t[y], w[x + y], w[x + y + 4]);
         // q2 > 0, or NaN (which the comparisons below ignore)
         const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * q2;
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
@@ -543,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         tmem_store16(at + 16, p);
         l += lo_f32(sum2) + hi_f32(sum2);
         // a value that is not finite, of a token that this row sees
-        if ((mt.bad[2 * hf] | mt.bad[2 * hf + 1]) != 0)
+        if (bad.x != 0)
           for (int x = 0; x < TH; ++x)
             if ((mt.bad[2 * hf + (x >> 5)] >> (x & 31)) & 1u)
               if (x >= lo && x <= hi) l = __int_as_float(0x7fffffff);
@@ -695,6 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
     load_scales(row, sc);
     load_codes(w, row_of(entry_of(0, first), 0, first));
     int e1 = entry_of(1, u), c1 = entry_of(1, first);  // the next tile's entries
+    build_pairs(smem_u32(smem + S::kOffTable), a.qtype, warp - kKeyWarp, 8);
+    ready();
     int run_exp = -100;  // values: exponent of the largest scale so far
     const int top_exp = value_top(a.qtype);
     for (int j = 0; j < T; ++j) {
@@ -852,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
     // to their end on whatever is there.
     const int r = warp - kIssueWarp;
     const uint32_t one = lane == 0 ? 1u : 0u;
+    ready();
     const uint32_t q_lo = desc_lo(q_at + r * S::kQ), k_lo = desc_lo(k_at), v_lo = desc_lo(v_at);
     auto product_s = [&](int i) {  // scores = q * keys: half i & 1 of tile i / 2
       const int j = i >> 1, hf = i & 1;
