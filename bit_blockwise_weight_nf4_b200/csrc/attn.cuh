@@ -110,6 +110,11 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // of the output against 4.3e-4).  FP4's magnitudes times 6 are E2M1's, exact.
 constexpr float kNf4Scale = 1613.0f / 1024.0f;
 constexpr float kFp4Scale = 6.0f;
+__device__ __forceinline__ float scaled_code(int qtype, int c) {
+  const float v = code_value_of(qtype, c);
+  // E2M1's magnitudes are multiples of a half
+  return qtype == kQtNF4 ? __fmul_rn(v, kNf4Scale) : rintf(__fmul_rn(v, 2.0f * kFp4Scale)) * 0.5f;
+}
 
 // Where row r of (sequence, key/value head) goes, divided by its sum of weights
 // (relative to 2^top).  A row that saw no token has top = -infinity and sum 0

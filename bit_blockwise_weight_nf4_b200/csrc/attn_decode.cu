@@ -99,8 +99,7 @@ template <bool KR>
 __device__ __forceinline__ void build_table(int qtype, int warp, int warps) {
   const int lane = threadIdx.x & 31;
   const int c = lane & 15;
-  const float v = qtype == kQtNF4 ? __fmul_rn(nf4_value(c), kNf4Scale)
-                                  : rintf(__fmul_rn(code_value(kQtFP4, c), 12.0f)) * 0.5f;
+  const float v = scaled_code(qtype, c);
   const uint32_t h = pack_f16x2(v, 0.0f) & 0xffffu;
   // exact: v is within half an fp16 step of h
   const uint32_t r = pack_f16x2(__fsub_rn(v, half_to_f32<BNB4_F16>(h)), 0.0f) & 0xffffu;

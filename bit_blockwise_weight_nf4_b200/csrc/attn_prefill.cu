@@ -255,8 +255,7 @@ __device__ __forceinline__ Lut make_residues(int qtype) {
 // t[byte & 15]} (times the table's constant), one copy per bank.
 __device__ __forceinline__ void build_pairs(uint32_t at, int qtype, int warp, int warps) {
   const int lane = threadIdx.x & 31, c = lane & 15;
-  const float v = qtype == kQtNF4 ? __fmul_rn(nf4_value(c), kNf4Scale)
-                                  : rintf(__fmul_rn(code_value(kQtFP4, c), 12.0f)) * 0.5f;
+  const float v = scaled_code(qtype, c);
   const uint32_t h = pack_f16x2(v, 0.0f) & 0xffffu;
 #pragma unroll 4
   for (int e = warp; e < 256; e += warps) {

@@ -45,6 +45,18 @@ __device__ __forceinline__ float code_value(int qtype, int c) {
   return (c & 8) ? -m : m;
 }
 
+// code_value of a code known only at run time, by selects: indexed, the table
+// would be put into local memory.
+__device__ __forceinline__ float code_value_of(int qtype, int c) {
+  float nf4 = 0.0f, fp4 = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    nf4 = c == j ? code_value(kQtNF4, j) : nf4;
+    fp4 = c == j ? code_value(kQtFP4, j) : fp4;
+  }
+  return qtype == kQtNF4 ? nf4 : fp4;
+}
+
 // Decoded absmax of block b: fma(u - 128, s, offset) rounded once with double
 // quantization, the exact absmax without.
 template <bool DQ>

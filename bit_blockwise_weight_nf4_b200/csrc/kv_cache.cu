@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvArgs a) {
   const int lane = threadIdx.x & 31, c = lane % LPR;
   // both halves of the warp hold the table: a lookup's index may carry one
   // bit more than the code
-  const float mine = code_value(a.qtype, lane & 15);
+  const float mine = code_value_of(a.qtype, lane & 15);
   pdl_wait();
   const uint32_t warps = gridDim.x * (kThreads / 32);
   const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
