@@ -20,8 +20,8 @@ struct AttnArgs {
   const int32_t *seq_lens, *cu_q;
   int64_t total_q;
   int batch, heads, group, max_q, num_pages, bt_width, causal, window, qtype;
-  int row_tiles;  // row tiles per (sequence, head); > 1 only without `split`
-  int split;      // the line of tiles is cut into equal runs
+  int row_tiles;  // the kernel for many rows: row tiles per (sequence, head)
+  int split;      // the other one: the line of tiles is cut into equal runs
   FastDiv page;
   float scale_log2;  // softmax scale * log2(e)
   float* ws;

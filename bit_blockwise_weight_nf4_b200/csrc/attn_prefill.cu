@@ -2,10 +2,31 @@
 // key/value cache on sm_100a (chunks of prompts): the tier of bnb_attn_4bit
 // for more than 16 rows (queries x grouped heads) per key/value head.
 //
+//   s_ij = scale * sum_d q_id t[k_code] a_k,  p_ij = exp(s_ij - m_i)
+//   o_id = sum_j p_ij t[v_code] a_v / sum_j p_ij
+// over the tokens j that row i sees, the running maximum m_i and the sums kept
+// in fp32 while the tokens pass once.
+//
 // Two matrix products on the tensor cores (tcgen05, fp16 in, fp32 sums in
 // tensor memory) around an online softmax, for tiles of 2 x 128 rows against
-// 128 tokens; what bounds it is the instruction issue and the exponentials of
-// the softmax, next to which the cache's decode has to fit.
+// 128 tokens.
+//
+// What bounds it (2 prompts of 2048 tokens, 32 heads of 128, bf16, NF4 blocks of
+// 64: 127 us, 543 TFLOP/s of the visible pairs' products; the products alone
+// would take 41 us).  A tile of 256 x 128 takes 5,100 cycles.  The softmax warps
+// are busy all of them but 580 -- 2,550 in the exponentials, which the two
+// warps of a scheduler share, the rest in the latencies of the loads from
+// tensor memory, maxima and hand-overs --, the warps that issue the products
+// wait 2,000 of them, and the decode's 4 + 4 warps 700 to 1,700.  The products
+// themselves need 2,700: with 64 columns at a time an operand of 6 KB is read
+// per 50 cycles, all that shared memory gives.  An item's start and end (page
+// table, first rows, q, first tile, output) cost 9 us, of which 3.5 items per
+// SM each pay their share.
+// Measured and not taken: more splits of the tokens than fill the SMs once
+// (slower by the join), the next half's scores loaded during this half's
+// weights (154 us: 96 registers a thread do not hold both), wholly unrolled
+// decoding and L2 prefetches of the codes (no difference), a CTA that walks
+// several items (slower: its turns bind the roles to one another).
 //
 // Roles of a CTA's 18 warps (one CTA per SM):
 //  * warps 0-3 and 4-7: the softmax of row tile 0 and 1, one row per thread.
@@ -28,6 +49,9 @@
 //    and the scores of the next one to take its columns.  (A wait, a commit
 //    and a product each cost the issuing warp around a hundred cycles: done by
 //    a softmax warp, or by one warp for both row tiles, they set the pace.)
+// Two row tiles share a CTA because the decode of a tile of keys and values
+// takes as long as the rest for 128 rows: 148 CTAs with 4352 tokens each take
+// 100 us for one row tile and 106 for both.
 // The stored order of a row's values is kept for K and q alike (a dot product
 // does not care) and undone when the output is written.
 //

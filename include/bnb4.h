@@ -1,8 +1,9 @@
 /*
  * bnb4.h -- C ABI of the B200 (sm_100a) library for 4-bit blockwise weight
  * quantization (NF4 / FP4), double quantization of the per-block absmax,
- * dequantization, and the fused 4-bit-weight x bf16-activation GEMV (decode)
- * and GEMM (prefill).
+ * dequantization, the fused 4-bit-weight x bf16-activation GEMV (decode)
+ * and GEMM (prefill), and the key/value cache of a decoder in the same 4 bits
+ * with the attention over it (at the end of this file).
  *
  * Sources, by page title and section:
  *  - CSDN article "bitsandbytes 是一个用于高效量化和加载大型语言模型（LLM）的开源库",

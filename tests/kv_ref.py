@@ -18,12 +18,17 @@ values).  For one output o = sum_j p_j V_jd with normalised weights p:
     |o - o64| <= (2 ds + et + ew + (n + 64) 2^-23) sum_j p_j |V_jd| * 1.1 + f
                  + u (|o64| + the same),
     u = 2^-8 (bf16) or 2^-11 (fp16) of the last rounding;
+  * the kernel for more than 16 rows multiplies table and scale before the
+    product, one rounding more of NF4's keys and values in fp16, 2^-11 (bf16
+    caches; FP4's 3 bits times a scale's 8 are exact, and fp16 caches keep what
+    is rounded away in a second term): added to et;
   * f = n 2^-39 max|V|: fp16 weights have an absolute step too.  A weight
     times its scale, p_j a_j <= a_max < 2^(e + 1), is rounded as p_j a_j 2^(14
     - e), below 2^-14 by at most half the subnormal step, 2^-25, that is
     2^(e - 39) <= 2^-39 a_max; times |t| <= 1 for each of n tokens, and p is
-    relative to the largest weight, so the sum it is divided by is >= 1.  (It
-    shows where the tokens that carry the row have a zero in a dimension.)
+    relative to the largest weight, so the sum it is divided by is >= 1.  (The
+    kernel for more than 16 rows holds p_j 2^7, so its step is 2^-25 2^-7 =
+    2^-32 of V.)  (It shows where the tokens that carry the row have a zero in a dimension.)
 On at least 1024 outputs the errors' root mean square adds in quadrature: bf16
 1.66e-3 (last rounding), 2.0e-4 (weights), 1e-4 (tables) < 2e-3; fp16 2.1e-4
 and 2.1e-4 (weights), 1.5e-4 (tables; scores of a size around one) < 5e-4:
@@ -132,7 +137,11 @@ def attention64(case, q, q_lens, causal=True, window=0, scale=None, rounded=2.0 
     bound = torch.zeros_like(o)
     lse = torch.full((T, nh), -math.inf, dtype=torch.float64)
     lse_b = torch.zeros_like(lse)
+    wide = group * max(q_lens) > 16
     et = TABLE_ERR[case.qtype]
+    if wide and case.qtype == bnb4.NF4 and case.dtype == oracle.BF16:
+        et += 2.0 ** -11
+    step = 2.0 ** (-32 if wide else -39)
     u = UNIT[case.dtype]
     at = 0
     for b, n in enumerate(q_lens):
@@ -158,7 +167,7 @@ def attention64(case, q, q_lens, causal=True, window=0, scale=None, rounded=2.0 
                     p = torch.softmax(s, -1)
                     o[at + i, h * group:(h + 1) * group] = p @ vv
                     rel = (2 * ds + et + rounded + (idx.numel() + 64) * 2.0 ** -23)[:, None]
-                    e = rel * (p @ vv.abs()) * 1.1 + idx.numel() * 2.0 ** -39 * vv.abs().max()
+                    e = rel * (p @ vv.abs()) * 1.1 + idx.numel() * step * vv.abs().max()
                     y = o[at + i, h * group:(h + 1) * group]
                     bound[at + i, h * group:(h + 1) * group] = e + u * (y.abs() + e)
                     lse[at + i, h * group:(h + 1) * group] = torch.logsumexp(s, -1)
