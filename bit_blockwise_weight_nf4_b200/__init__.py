@@ -626,7 +626,8 @@ def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None
     see bnb_attn_4bit in include/bnb4.h.  ``block_table`` int32 [B, W] (pages
     of each sequence), ``seq_lens`` int32 [B] (its cached tokens, the queries'
     own among them).  The queries are ragged by ``cu_seqlens_q`` (int32 [B +
-    1], with ``max_q_len``), or T / B for each sequence.  ``scale`` defaults
+    1], with ``max_q_len``, by which the kernel is chosen: T unless given), or T /
+    B for each sequence.  ``scale`` defaults
     to 1 / sqrt(D); ``window`` > 0 limits how far back a query sees;
     ``lse`` (fp32 [T, heads], contiguous) receives the log-sum-exp.
     ``max_seq_len`` (default: what the block table holds) is the bound by

@@ -40,6 +40,14 @@ int check_strides(int64_t ts, int64_t hs, int64_t per) {
   return ts % per == 0 && hs % per == 0 ? BNB4_OK : BNB4_ERR_ALIGNMENT;
 }
 
+// Rows that are written do not lie over one another.
+int check_written(int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t dim,
+                  int64_t per) {
+  const int rc = check_strides(ts, hs, per);
+  if (rc != BNB4_OK) return rc;
+  return (tokens > 1 && ts < dim) || (heads > 1 && hs < dim) ? BNB4_ERR_SHAPE : BNB4_OK;
+}
+
 int on_device(const void* p) {
   const void* d;
   return bnb4::resolve_ptr(p, bnb4::Residency::kDevice, &d);
@@ -97,8 +105,11 @@ int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, int64_t t
   if (!k && !v) return BNB4_ERR_INVALID_ARG;
   if ((rc = check_rows(tokens, slots, cache)) != BNB4_OK) return rc;
   const int64_t per = out_dtype == BNB4_F32 ? 4 : 8;
-  if (k && (rc = check_strides(k_stride_t, k_stride_h, per)) != BNB4_OK) return rc;
-  if (v && (rc = check_strides(v_stride_t, v_stride_h, per)) != BNB4_OK) return rc;
+  const int64_t heads = cache->n_kv_heads, dim = cache->head_dim;
+  if (k && (rc = check_written(k_stride_t, k_stride_h, tokens, heads, dim, per)) != BNB4_OK)
+    return rc;
+  if (v && (rc = check_written(v_stride_t, v_stride_h, tokens, heads, dim, per)) != BNB4_OK)
+    return rc;
   if (!aligned(k, 16) || !aligned(v, 16)) return BNB4_ERR_ALIGNMENT;
   int sms;
   if ((rc = bnb4::device_sms(&sms)) != BNB4_OK) return rc;
@@ -149,7 +160,9 @@ int bnb_attn_4bit(const bnb4_attn* a, void* stream) {
   if (a->batch == 0 || a->total_q == 0) return BNB4_OK;
   if (!a->q || !a->out || !a->block_table || !a->seq_lens) return BNB4_ERR_INVALID_ARG;
   if ((rc = check_strides(a->q_stride_t, a->q_stride_h, 8)) != BNB4_OK) return rc;
-  if ((rc = check_strides(a->out_stride_t, a->out_stride_h, 8)) != BNB4_OK) return rc;
+  if ((rc = check_written(a->out_stride_t, a->out_stride_h, a->total_q, a->n_heads,
+                          a->cache->head_dim, 8)) != BNB4_OK)
+    return rc;
   if (!aligned(a->q, 16) || !aligned(a->out, 16) || !aligned(a->block_table, 4) ||
       !aligned(a->seq_lens, 4) || !aligned(a->cu_seqlens_q, 4) || !aligned(a->lse, 4))
     return BNB4_ERR_ALIGNMENT;

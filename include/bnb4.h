@@ -434,7 +434,8 @@ BNB4_API int bnb_kv_write_4bit(const void* k, int64_t k_stride_t, int64_t k_stri
  * The cached keys and values of `tokens` slots, dequantized to out_dtype
  * (BNB4_F32, BNB4_BF16 or BNB4_F16): RN_out(RN(t[code] * absmax)).  k or v
  * may be NULL (not read).  Rows of a slot outside the cache are left as they
- * were.  Strides in elements, >= 0, multiples of 8 (4 for BNB4_F32).
+ * were.  Strides in elements, >= head_dim where there is more than one token
+ * or head, multiples of 8 (4 for BNB4_F32).
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, SHAPE, CUDA.
  */
 BNB4_API int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, int64_t tokens,
@@ -450,8 +451,8 @@ BNB4_API int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, 
  * seq_lens[b] - n_b + i and sees the tokens j < seq_lens[b] with, if causal,
  * j <= p and, if window > 0, j > p - window:
  *   out = sum_j softmax_j(scale * q . K_j) V_j
- * with K and V the cached values, unrounded, sums in fp32 and one rounding to
- * dtype.  Head h of n_heads attends to key/value head h / (n_heads /
+ * with K and V the cached values (held in fp16 times a power of two, in two
+ * terms where dtype is fp16), sums in fp32 and one rounding to dtype.  Head h of n_heads attends to key/value head h / (n_heads /
  * n_kv_heads).  A query that sees nothing (an empty sequence, one shorter
  * than its queries) gives zeros and a log-sum-exp of -infinity.
  *  cu_seqlens_q  int32[batch + 1]: sequence b's queries are rows
@@ -468,8 +469,10 @@ BNB4_API int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, 
  *          exp(scale * q . K_j), or NULL.
  *  workspace     bnb4_attn_workspace bytes (0: may be NULL), 16-byte aligned,
  *          any contents; not to be shared by calls that may overlap.
- * All device memory; q and out 16-byte aligned, strides in elements, >= 0,
- * multiples of 8.  Finite scales are taken up to 2^100.  Results repeat bit
+ * All device memory; q and out 16-byte aligned, strides in elements, >= 0
+ * (out: >= head_dim where there is more than one row or head), multiples of 8.
+ * Finite scales are taken up to 2^100; a scale that is not finite makes the
+ * rows that see its token NaN.  Results repeat bit
  * for bit on a device.  The call reads seq_lens, cu_seqlens_q and block_table
  * on the device, so a captured graph may be replayed with other lengths.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, SHAPE, WORKSPACE, CUDA.

@@ -77,6 +77,8 @@ def test_read_errors():
     assert call(kt=250) == bnb4.ERR_ALIGNMENT and call(kt=-4) == bnb4.ERR_SHAPE
     assert call(kt=252, dt=bnb4.BF16) == bnb4.ERR_ALIGNMENT
     assert call(k=None, kt=3, v=A + 4) == bnb4.ERR_ALIGNMENT
+    # rows that would lie over one another
+    assert call(n=2, kt=64) == bnb4.ERR_SHAPE and call(vh=64) == bnb4.ERR_SHAPE
     assert call(n=1 << 30) == bnb4.ERR_SHAPE
 
 
@@ -106,6 +108,7 @@ def attn(**kw):
     (dict(n_heads=0), bnb4.ERR_SHAPE), (dict(total_q=4), bnb4.ERR_SHAPE),
     (dict(block_table_width=0), bnb4.ERR_SHAPE), (dict(block_table_stride=7), bnb4.ERR_SHAPE),
     (dict(q_stride_t=-8), bnb4.ERR_SHAPE), (dict(q_stride_t=12), bnb4.ERR_ALIGNMENT),
+    (dict(out_stride_h=0), bnb4.ERR_SHAPE), (dict(out_stride_t=64), bnb4.ERR_SHAPE),
     (dict(out_stride_h=4), bnb4.ERR_ALIGNMENT), (dict(q=A + 8), bnb4.ERR_ALIGNMENT),
     (dict(out=A + 2), bnb4.ERR_ALIGNMENT), (dict(lse=A + 2), bnb4.ERR_ALIGNMENT),
     (dict(seq_lens=A + 1), bnb4.ERR_ALIGNMENT), (dict(cu_seqlens_q=A + 2), bnb4.ERR_ALIGNMENT),
