@@ -60,7 +60,9 @@
 // the scores --, values by a running power of two, to at most 2^16, and weights
 // by 2^7 (so at most 2^15): both stay normal 21 binades and more below the
 // largest.  For fp16 caches, whose outputs' last place is finer than those
-// roundings, keys and values are kept in two fp16 terms (twice the products).
+// roundings, keys, values and weights are kept in two fp16 terms (twice the
+// products for the scores, three times for the sums; in one term the weights'
+// rounding made up to 1.56 times the error of exact fp32 weights).
 // Every mbarrier wait is bounded; no TMA load is used.
 #include "attn.cuh"
 #include "common.cuh"
@@ -579,12 +581,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
             const float e0 = ex2(lo_f32(z)), e1 = ex2(hi_f32(z));
             sum2 = add_f32x2(sum2, pair_f32(e0, e1));
             p[x / 2] = pack_f16x2(e0, e1);
+            if constexpr (HL) y[x] = e0, y[x + 1] = e1;
           }
+        };
+        // what the weights' fp16 rounding left, over the other half of the scores
+        auto rest = [&](const float (&y)[32]) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 2)
+            p[x / 2] = pack_f16x2(y[x] - half_to_f32<BNB4_F16>(p[x / 2] & 0xffffu),
+                                  y[x + 1] - half_to_f32<BNB4_F16>(p[x / 2] >> 16));
         };
         weights(v);
         tmem_store16(at, p);
+        if constexpr (HL) {
+          rest(v);
+          tmem_store16(at + TH / 2, p);
+        }
         weights(w);
         tmem_store16(at + 16, p);
+        if constexpr (HL) {
+          rest(w);
+          tmem_store16(at + TH / 2 + 16, p);
+        }
         l += lo_f32(sum2) + hi_f32(sum2);
         // a value that is not finite, of a token that this row sees
         if (bad.x != 0)
@@ -932,6 +950,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         for (int k = 0; k < TH / 16; ++k)
           umma_ts(one, o_col(r), s_col(r) + TH * hf + 8 * k, v + S::kVTerm / 16 + 2 * k, kIdescO,
                   1u);
+#pragma unroll
+        for (int k = 0; k < TH / 16; ++k)  // the weights' second term
+          umma_ts(one, o_col(r), s_col(r) + TH * hf + TH / 2 + 8 * k, v + 2 * k, kIdescO, 1u);
       }
       if (hf) umma_commit(one, bar(ctl->v_empty[j % kStages]));
     };

@@ -12,7 +12,7 @@ values).  For one output o = sum_j p_j V_jd with normalised weights p:
     order; exp2 by 2^-22 of the weight plus the rounding of its argument,
     2^-23 of |s|;
   * a weight is rounded to fp16: 2^-11 of itself (fp16 caches: both halves
-    kept, 2^-22; the tensor-core prefill kernel rounds in either type);
+    kept, 2^-22);
   * so with ds = the largest score error of the row, every weight is off by a
     factor within exp(2 ds) and
     |o - o64| <= (2 ds + et + ew + (n + 64) 2^-23) sum_j p_j |V_jd| * 1.1 + f

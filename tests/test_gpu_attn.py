@@ -330,3 +330,20 @@ def test_operators():
     cu = ints([0, 0, 1])
     y = torch.ops.bnb4.attn_4bit(q, *ts, bt, sl, cu, 1, 90, 0.125, True, 0, 32, bnb4.FP4)
     assert (y[1] == 0).all() and not (y[0] == 0).all()
+
+
+@pytest.mark.parametrize("D,bs", [(64, 32), (128, 64)])
+@pytest.mark.parametrize("qtype", [bnb4.NF4, bnb4.FP4])
+def test_fp16_chunks_lose_only_the_last_rounding(D, bs, qtype):
+    """fp16, many rows, weights on a few tokens: keys, values and weights are held
+    in two fp16 terms (2^-22 each), so the error is the output's last rounding.
+    Half a step is 2^-11 / m of a value with mantissa m, uniform: 2^-11 / sqrt(3)
+    sqrt(E m^-2) = 2^-11 * 0.577 * 0.736 = 2.07e-4 in the mean square for evenly
+    spread logarithms (E m^-2 = 3 / (8 ln 2)); 10% more for 10240 samples that
+    are not quite that, and for the fp32 sums."""
+    case = Case([600], 32, 2, D, bs, qtype, oracle.F16, seed=D + bs)
+    q = case.queries(40, 4, std=2.0)
+    out, _ = run(case, q, [40])
+    o64, _, _, _ = attention64(case, q, [40])
+    rel = float((out.cpu().double() - o64).norm() / o64.norm())
+    assert rel <= 2.28e-4, rel
