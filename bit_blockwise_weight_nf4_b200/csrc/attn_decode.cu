@@ -480,8 +480,13 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[n][s][0] = raw[n][s][0], qf[n][s][1] = raw[n][s][1];
       }
-      // a row with an infinite or NaN entry is NaN, whatever its products are
-      if (top >= (F == BNB4_BF16 ? 0x7f80u : 0x7c00u)) mul = __int_as_float(0x7fffffff);
+      // a row with an infinite or NaN entry is NaN as a whole, so every score of a
+      // token that it sees is; `mul` stays finite, so that a token that it does not
+      // see keeps its weight of zero
+      if (top >= kInf) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[n][s][0] = qf[n][s][1] = 0x7fff7fffu;
+      }
       mul *= a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale;
       // columns 2 t and 2 t + 1 are rows held by lanes 4 (2 t) and 4 (2 t + 1)
       qs[n][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
@@ -633,7 +638,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
           for (int u = 0; u < NS; ++u) x = fmaxf(x, fmaxf(s[u][n][c], s[u][n][c + 2]));
 #pragma unroll
           for (int y = 4; y <= 16; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
-          top[n][c] = fmaxf(m[n][c], x * qs[n][c]);  // qs > 0 (or NaN, which m ignores)
+          top[n][c] = fmaxf(m[n][c], x * qs[n][c]);  // qs > 0; drops NaN
         }
       wait(got, true);
       Scales<NB> vs[NS][2];

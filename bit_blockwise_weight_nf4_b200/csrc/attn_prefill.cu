@@ -468,6 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
                            pack_f16x2(bf16_lo(v.z) * f, bf16_hi(v.z) * f),
                            pack_f16x2(bf16_lo(v.w) * f, bf16_hi(v.w) * f));
           }
+          // a row with an infinite or NaN entry is NaN as a whole: see attn_decode.cu
+          if (t >= (F == BNB4_BF16 ? 0x7f80u : 0x7c00u))
+            v = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
           const int rw = y * kPer + sub;
           *reinterpret_cast<uint4*>(dst + rw * 128 + (((c & 7) ^ (rw & 7)) << 4)) = v;
           const uint32_t own = __shfl_sync(0xffffffffu, t, (lane % kPer) * (D / 8));
@@ -477,7 +480,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           int e = static_cast<int>(top >> 7) - 127;
           qs *= pow2((e < -100 ? -100 : e) - 14);
         }
-        if (top >= (F == BNB4_BF16 ? 0x7f80u : 0x7c00u)) qs = __int_as_float(0x7fffffff);
         qs *= a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         for (int x = 0; x < 32; x += 8)
 #pragma unroll
           for (int y = 0; y < 4; ++y) t[y] = max3(t[y], w[x + y], w[x + y + 4]);
-        // q2 > 0, or NaN (which the comparisons below ignore)
+        // q2 > 0; a row of NaN scores has no maximum
         const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * q2;
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
         const bool shift = i2 > 0 && tve != ve;
