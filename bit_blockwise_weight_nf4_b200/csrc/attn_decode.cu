@@ -466,6 +466,12 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       float mul = a.scale_log2;
+      // a row with an infinite or NaN entry is NaN as a whole, so every score of a
+      // token that it sees is; `mul` stays finite, so that a token that it does not
+      // see keeps its weight of zero
+      const uint32_t poison = top >= kInf ? 0x7fff7fffu : 0u;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) raw[n][s][0] |= poison, raw[n][s][1] |= poison;
       if constexpr (F == BNB4_BF16) {
         int e = static_cast<int>(top >> 7) - 127;  // exponent of the row's largest
         e = e < -100 ? -100 : e;
@@ -479,13 +485,6 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
       } else {
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[n][s][0] = raw[n][s][0], qf[n][s][1] = raw[n][s][1];
-      }
-      // a row with an infinite or NaN entry is NaN as a whole, so every score of a
-      // token that it sees is; `mul` stays finite, so that a token that it does not
-      // see keeps its weight of zero
-      if (top >= kInf) {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) qf[n][s][0] = qf[n][s][1] = 0x7fff7fffu;
       }
       mul *= a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale;
       // columns 2 t and 2 t + 1 are rows held by lanes 4 (2 t) and 4 (2 t + 1)
