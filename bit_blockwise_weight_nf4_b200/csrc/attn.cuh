@@ -103,6 +103,10 @@ __device__ __forceinline__ float lg2(float x) {
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
+// A score (in binades) below which half a step of its last place, 2^-8, leaves a
+// weight's size as it is.
+constexpr float kFarScore = 65536.0f;
+
 // The code table times this constant rounds to fp16 within 3.1e-4 of a value,
 // exactly at the block's largest (1 and -1), with a root mean square error of
 // 3.6e-5 of the scale (as it stands: 7e-5); of the constants with exact ends

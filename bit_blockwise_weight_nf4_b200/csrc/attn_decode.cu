@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
           for (int u = 0; u < NS; ++u) x = fmaxf(x, fmaxf(s[u][n][c], s[u][n][c + 2]));
 #pragma unroll
           for (int y = 4; y <= 16; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
-          top[n][c] = fmaxf(m[n][c], x * qs[n][c]);  // qs > 0; drops NaN
+          top[n][c] = fmaxf(m[n][c], __fmul_rn(x, qs[n][c]));  // qs > 0; drops NaN
         }
       wait(got, true);
       Scales<NB> vs[NS][2];
@@ -733,6 +733,31 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) ref[n][c] = m[n][c] == -INFINITY ? 0.0f : m[n][c];
+      // Scores to the weights' exponents.  Where they are so large that half a step
+      // of theirs counts, the product is rounded as the maximum's was before the
+      // maximum is taken off, so that the largest weight is one (an fma would
+      // leave that half step).
+      bool far = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) far = far || fmaxf(fabsf(ref[n][0]), fabsf(ref[n][1])) > kFarScore;
+      if (__any_sync(0xffffffffu, far)) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              s[u][n][c] = __fsub_rn(__fmul_rn(s[u][n][c], qs[n][c & 1]), ref[n][c & 1]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              s[u][n][c] = fmaf(s[u][n][c], qs[n][c & 1], -ref[n][c & 1]);
+      }
       // ------------------------------------------------ weights and values
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
@@ -747,7 +772,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
           float p[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            p[c] = ex2(fmaf(s[u][n][c], qs[n][c & 1], -ref[n][c & 1]));
+            p[c] = ex2(s[u][n][c]);
             l[n][c & 1] += p[c];
           }
 #pragma unroll

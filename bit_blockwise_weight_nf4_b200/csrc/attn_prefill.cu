@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
 #pragma unroll
           for (int y = 0; y < 4; ++y) t[y] = max3(t[y], w[x + y], w[x + y + 4]);
         // q2 > 0; a row of NaN scores has no maximum
-        const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]) * q2;
+        const float top = __fmul_rn(fmaxf(max3(t[0], t[1], t[2]), t[3]), q2);
         const bool grow = top > m + kLazy || (m == -INFINITY && top > m);
         const bool shift = i2 > 0 && tve != ve;
         if (__any_sync(0xffffffffu, grow) || shift) {
@@ -573,9 +573,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           }
         }
         ve = tve;
-        const float ref = (m == -INFINITY ? 0.0f : m) - static_cast<float>(kBoost);
+        float ref = m == -INFINITY ? 0.0f : m, mul = q2;
+        // Scores so large that half a step of theirs counts: the product is rounded
+        // as the maximum's was, before the maximum is taken off, so that weights
+        // stay within 2^kLazy (the fma below would leave that half step).
+        if (__any_sync(0xffffffffu, fabsf(ref) > kFarScore)) {
+          asm volatile("" ::: "memory");  // a branch
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            v[x] = __fsub_rn(__fmul_rn(v[x], q2), ref);
+            w[x] = __fsub_rn(__fmul_rn(w[x], q2), ref);
+          }
+          ref = 0.0f, mul = 1.0f;
+        }
+        ref -= static_cast<float>(kBoost);
         uint64_t sum2 = 0;  // two sums of the weights
-        const uint64_t q22 = pair_f32(q2, q2), ref2 = pair_f32(-ref, -ref);
+        const uint64_t q22 = pair_f32(mul, mul), ref2 = pair_f32(-ref, -ref);
         uint32_t p[16];
         auto weights = [&](float (&y)[32]) {
 #pragma unroll
