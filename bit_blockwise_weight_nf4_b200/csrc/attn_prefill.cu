@@ -56,10 +56,10 @@
 // does not care) and undone when the output is written.
 //
 // Precision.  q as in the decode kernel; keys are rounded to fp16 after
-// scaling by the tile's largest scale's power of two -- an absolute error in
-// the scores --, values by a running power of two, to at most 2^16, and weights
-// by 2^7 (so at most 2^15): both stay normal 21 binades and more below the
-// largest.  For fp16 caches, whose outputs' last place is finer than those
+// scaling by the power of two of their tile's largest scale, values by a running
+// one, both to at most 2^16, and weights by 2^7 (so at most 2^15): keys and values
+// stay normal 24 binades below the largest, whether a row sees that one or not,
+// weights 21.  For fp16 caches, whose outputs' last place is finer than those
 // roundings, keys, values and weights are kept in two fp16 terms (twice the
 // products for the scores, three times for the sums; in one term the weights'
 // rounding made up to 1.56 times the error of exact fp32 weights).  The prompts
@@ -85,9 +85,11 @@ constexpr int kMaxStages = 2;
 constexpr int kRing = 4;       // tiles' scalars: see Meta
 constexpr float kLazy = 8.0f;  // growth of the maximum that is let pass, in binades
 constexpr int kBoost = 7;      // weights are held times 2^kBoost
-// Values are held times 2^(top - exponent of the largest scale): NF4's table
-// ends at 1.58, FP4's at 6, so at most 5.2e4 in fp16.
-__host__ __device__ constexpr int value_top(int qtype) { return qtype == kQtNF4 ? 14 : 12; }
+// Keys and values are held times 2^(top - exponent of the largest scale): NF4's
+// table ends at 1.58, FP4's at 6, so at most 5.2e4 in fp16, and normal down to
+// 2^-25 of the largest scale.  (A score of 128 such products with q, below 2^16,
+// stays below 2^40.)
+__host__ __device__ constexpr int held_top(int qtype) { return qtype == kQtNF4 ? 14 : 12; }
 constexpr int kHalf = TK * 128;  // 128 rows of 128 bytes
 
 // HL: keys and values are held in two fp16 terms each (fp16 caches: see the
@@ -636,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       }
       {
-        const float back = pow2(ve - value_top(a.qtype)) *
+        const float back = pow2(ve - held_top(a.qtype)) *
                            (a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale);
         const float lse_top = m - static_cast<float>(kBoost);
         const bool sees = m != -INFINITY || l != 0.0f;
@@ -776,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
     build_pairs(smem_u32(smem + S::kOffTable), a.qtype, warp - kKeyWarp, 8);
     ready();
     int run_exp = -100;  // values: exponent of the largest scale so far
-    const int top_exp = value_top(a.qtype);
+    const int top_exp = held_top(a.qtype);
     for (int j = 0; j < T; ++j) {
       const int s = j % kStages;
       // the next tile's loads are on their way while this one is decoded
@@ -809,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
       int e = F == BNB4_BF16 ? static_cast<int>(top >> 7) - 127 : static_cast<int>(top >> 10) - 15;
       e = e < -100 ? -100 : e;
       if (values) e = run_exp = e > run_exp ? e : run_exp;
-      const float norm = pow2(values ? top_exp - e : -e);
+      const float norm = pow2(top_exp - e);
       // fp16 factors; a key row with a scale that is not finite becomes NaN, a
       // value row zero (the rows that see it are made NaN by the softmax)
       uint32_t fac[NB];
@@ -831,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
           if ((warp & 3) == 0) mt.value_exp = e;
         } else {
           mt.present[warp & 3] = static_cast<uint8_t>((have & 1u) | ((have >> 15) & 2u));
-          if ((warp & 3) == 0) mt.key_exp = e;
+          if ((warp & 3) == 0) mt.key_exp = e - top_exp;
         }
         mbar_arrive(bar(ctl->m_full[j % kRing]));
       }

@@ -4,10 +4,47 @@ import torch
 
 import bit_blockwise_weight_nf4_b200 as bnb4
 import oracle
-from kv_ref import TORCH, Case, attention64, quantize_rows
+from kv_ref import TORCH, Case, attention64, check, quantize_rows
 from test_gpu_attn import run
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,small,binades", [(oracle.BF16, 1.0, 8), (oracle.BF16, 1.0, 16),
+                                                 (oracle.BF16, 2.0 ** -40, 24),
+                                                 (oracle.F16, 2.0 ** -6, 16)])
+@pytest.mark.parametrize("qtype", [bnb4.NF4, bnb4.FP4])
+@pytest.mark.parametrize("q_len,window", [(3, 0), (40, 0), (40, 30), (200, 150)])
+def test_a_large_key_that_a_row_does_not_see(q_len, window, qtype, dtype, small, binades):
+    """Two tokens' keys are up to 2^24 times the others': the rows before them,
+    and those whose window has left them, are as exact as without them.  (A
+    key in the chunk kernel is normal fp16 over 24 binades below the largest
+    of its tile, so the module's bounds hold as they stand.)"""
+    lens = [333, 61]
+    case = Case(lens, 32, 2, 128, 64, qtype, dtype, seed=binades, k_std=small)
+    untouched = []  # rows that see neither of the two
+    for kv in lens:
+        large = (kv - 1, max(0, kv - 170) if q_len == 200 else kv - q_len // 2 - 1)
+        b = lens.index(kv)
+        for j in large:
+            page, at = int(case.block_table[b, j // 32]), j % 32
+            row = torch.randn(2, 128, generator=case.gen) * small * 2.0 ** binades
+            case.k_codes[page, :, at], case.k_absmax[page, :, at], _ = \
+                quantize_rows(row.to(TORCH[dtype]), 64, qtype)
+        for pos in range(kv - q_len, kv):
+            untouched.append(not any(j <= pos and (not window or j > pos - window)
+                                     for j in large))
+    untouched = torch.tensor(untouched)
+    assert untouched.any()
+    q = case.queries(2 * q_len, 4, std=1.0 if dtype == oracle.F16 else 1.0 / small)
+    out, lse = run(case, q, [q_len] * 2, window=window)
+    o64, bound, l64, lb = attention64(case, q, [q_len] * 2, window=window)
+    # (of the other rows only the log-sum-exp is checked: the bound of an output is
+    # linear in the scores' error, which is not small next to a score of 2^24)
+    assert torch.isfinite(out).all()
+    check(out.cpu()[untouched], o64[untouched], bound[untouched], case.dtype)
+    seen = ~torch.isinf(l64)
+    assert ((lse.cpu().double() - l64).abs()[seen] <= lb[seen]).all()
 
 
 @pytest.mark.parametrize("dtype", [oracle.BF16, oracle.F16])
