@@ -43,7 +43,7 @@ F32 = 0
 BF16 = 1
 F16 = 2
 
-ABI_VERSION = 5
+ABI_VERSION = 6
 GROUP_MAX = 256
 
 
@@ -139,6 +139,7 @@ def load():
         "bnb_attn_4bit": ([ctypes.POINTER(Attn), p], ctypes.c_int),
         "bnb4_device_status": ([p, i32], ctypes.c_int),
         "bnb4_debug_gemm_withhold": ([p, i64, i64, QP, i64, p, i32, p], ctypes.c_int),
+        "bnb4_debug_attn_withhold": ([ctypes.POINTER(Attn), i32, p], ctypes.c_int),
         "bnb4_debug_check_rcp": ([p, p], ctypes.c_int),
         "bnb4_strerror": ([ctypes.c_int], ctypes.c_char_p),
         "bnb4_abi_version": ([], ctypes.c_int),
@@ -241,6 +242,11 @@ def bnb4_attn_workspace(args):
 
 def bnb_attn_4bit(args, stream):
     return load().bnb_attn_4bit(ctypes.byref(args), stream)
+
+
+def bnb4_debug_attn_withhold(args, wait_limit_us, stream):
+    """Failure-detection diagnostic (see include/bnb4.h)."""
+    return load().bnb4_debug_attn_withhold(ctypes.byref(args), wait_limit_us, stream)
 
 
 def bnb4_debug_gemm_withhold(X, M, K, W, N, Y, wait_limit_us, stream):

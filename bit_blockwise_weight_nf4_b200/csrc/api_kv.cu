@@ -154,7 +154,7 @@ int bnb4_attn_workspace(const bnb4_attn* a, size_t* bytes) {
   return BNB4_OK;
 }
 
-int bnb_attn_4bit(const bnb4_attn* a, void* stream) {
+static int run_attn(const bnb4_attn* a, void* stream, uint64_t wait_limit_ns, int withhold) {
   int rc = check_attn(a);
   if (rc != BNB4_OK) return rc;
   if (a->batch == 0 || a->total_q == 0) return BNB4_OK;
@@ -182,7 +182,15 @@ int bnb_attn_4bit(const bnb4_attn* a, void* stream) {
   if ((rc = check_cache_memory(a->cache)) != BNB4_OK) return rc;
   int* err;
   if ((rc = bnb4::device_error_word(&err)) != BNB4_OK) return rc;
-  return from_cuda(bnb4::launch_attn(*a, sms, err, static_cast<cudaStream_t>(stream)));
+  return from_cuda(bnb4::launch_attn(*a, sms, err, static_cast<cudaStream_t>(stream),
+                                     wait_limit_ns, withhold));
+}
+
+int bnb_attn_4bit(const bnb4_attn* a, void* stream) { return run_attn(a, stream, 0, 0); }
+
+int bnb4_debug_attn_withhold(const bnb4_attn* a, int32_t wait_limit_us, void* stream) {
+  if (wait_limit_us < 1 || wait_limit_us > 1000000) return BNB4_ERR_INVALID_ARG;
+  return run_attn(a, stream, static_cast<uint64_t>(wait_limit_us) * 1000u, 1);
 }
 
 }  // extern "C"

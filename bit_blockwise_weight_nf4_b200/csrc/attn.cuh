@@ -26,6 +26,8 @@ struct AttnArgs {
   float scale_log2;  // softmax scale * log2(e)
   float* ws;
   int* err;
+  uint64_t wait_limit_ns;
+  int withhold;  // failure-detection diagnostic: CTA 0 waits for what never comes
 };
 
 // The tensor-core kernel for tiles of 2 x 128 rows (attn_prefill.cu): `rows`

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (threadIdx.x == 0) {
-    ctl.wait_limit_ns = kWaitLimitNs;
+    ctl.wait_limit_ns = a.wait_limit_ns;
     ctl.abort = 0;
   }
   // the table is built by the warps that do not look for their group's run below
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
   const uint8_t* copy_k = lane & 1 ? reinterpret_cast<const uint8_t*>(a.k_absmax) : a.k_codes;
   const uint8_t* copy_v = lane & 1 ? reinterpret_cast<const uint8_t*>(a.v_absmax) : a.v_codes;
   uint32_t put = 0, got = 0;  // tiles issued and consumed; slot = count % ST
-  bool ok_all = true;         // no wait gave up
+  bool ok_all = true;         // no wait of this warp gave up
 
   // The group's segments: the pair (b, h) and its tiles tile0 .. tile1 - 1.
   struct Seg {
@@ -379,22 +379,25 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
                ? (static_cast<int64_t>(entry) * a.heads + w.h) * a.page.d + in
                : static_cast<int64_t>(-1);
   };
-  // into slot n % ST; returns bit 2 u for each sub-tile u that is there
-  auto issue = [&](int64_t row, uint32_t n, bool values) {
+  // into slot n % ST; returns bit 2 u for each sub-tile u that is there.  hold: the
+  // lane's copy is counted but not made (failure-detection diagnostic).
+  auto issue = [&](int64_t row, uint32_t n, bool values, bool hold = false) {
     const uint32_t at = (values ? my_v : my_k) + (n % ST) * S::kStage + copy_at;
     const uint32_t bar = smem_u32(&bars[warp][(values ? ST : 0) + n % ST]);
     const unsigned have = __ballot_sync(0xffffffffu, row >= 0) & 0x55555555u;
     if (lane == 0)
       mbar_arrive_expect_tx(bar, __popc(have) * (S::kCodes / NS + S::kScales / NS));
     __syncwarp();  // also orders the slot's last reads before the copies
-    if (row >= 0)
+    if (row >= 0 && !hold)
       copy_to_shared(at, (values ? copy_v : copy_k) + row * copy_row, copy_bytes, bar);
     return have;
   };
   auto wait = [&](uint32_t n, bool values) {
     const uint32_t bar = smem_u32(&bars[warp][(values ? ST : 0) + n % ST]);
-    if (!wait_bounded(bar, (n / ST) & 1, &ctl, a.err)) ok_all = false;
-    __syncwarp();
+    // Every lane asks for itself, and one may see the phase complete where another
+    // sees that the CTA gives up: the warp decides as one, since all that it does
+    // next (votes, shuffles, products) takes all its lanes.
+    if (!__all_sync(0xffffffffu, wait_bounded(bar, (n / ST) & 1, &ctl, a.err))) ok_all = false;
   };
 
   // Starts a segment: its first tiles are on their way, and its rows of q (as B
@@ -436,7 +439,8 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
       if (i < w.tile1 && ok_all) {  // after a failed wait nothing more is issued, but
                                     // the group's barriers below are still met
         const int64_t row = row_of(w, i, entry[x]);
-        have |= issue(row, put, false) << (2 * NS * x);
+        have |= issue(row, put, false, a.withhold && blockIdx.x == 0 && threadIdx.x == 1)
+                << (2 * NS * x);
         issue(row, put, true);
         ++put;
       }
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
       // the next tile's keys are on their way while this one's weights form
       const bool more = i + ST * GW < tile1;
       int64_t row_next = -1;
-      if (more) {
+      if (more && ok_all) {
         row_next = row_of(cur, i + ST * GW, entry_next);
         have |= issue(row_next, put, false) << (2 * NS * (ST - 1));
       }
@@ -816,6 +820,7 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
                 pair_of<3>(ev1, lane_base), pair_of<3>(od1, lane_base));
         }
       }
+      if (!ok_all) break;  // what is in flight is waited for below
       ++got;
       if (more) {
         issue(row_next, put, true);
@@ -938,7 +943,8 @@ __global__ void __launch_bounds__(Shape<D, BS, F, NT, KR>::W * 32, 1)
       }
     group_sync(grp, GW * 32);  // the shared arrays are free for the next segment
   }
-  // a wait that gave up: copies in flight land before the CTA ends
+  // a wait that gave up: copies in flight (of tile `put` the keys at most) land
+  // before the CTA ends
   if (!ok_all)
     for (uint32_t n = got; n < put + 1; ++n)
       for (int v = 0; v < 2; ++v)
@@ -1155,11 +1161,14 @@ size_t attn_workspace_bytes(const bnb4_attn& p) {
   return sizeof(float) * 2 * kMaxRuns * rt * (static_cast<size_t>(p.cache->head_dim) + 2);
 }
 
-cudaError_t launch_attn(const bnb4_attn& p, int num_sms, int* err, cudaStream_t s) {
+cudaError_t launch_attn(const bnb4_attn& p, int num_sms, int* err, cudaStream_t s,
+                        uint64_t wait_limit_ns, int withhold) {
   const bnb4_kv_cache& c = *p.cache;
   int64_t rows, span;
   AttnArgs a = args_of(p, &rows, &span);
   a.err = err;
+  a.wait_limit_ns = wait_limit_ns ? wait_limit_ns : kWaitLimitNs;
+  a.withhold = withhold;
   if (rows > kMaxRows) return launch_attn_prefill(a, c, rows, span, kSms, s);
   const int rt = rows <= 8 ? 8 : 16;
 #define BNB4_ATTN(DV, BSV)                                                               \

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
     }
     for (int s = 0; s < kRing; ++s) mbar_init(bar(ctl->m_full[s]), 8);
     ctl->abort = 0;
-    ctl->wait_limit_ns = kWaitLimitNs;
+    ctl->wait_limit_ns = a.wait_limit_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         qs *= a.qtype == kQtNF4 ? 1.0f / kNf4Scale : 1.0f / kFp4Scale;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(ctl->q_full[r]));
+        if (lane == 0 && !(a.withhold && blockIdx.x == 0 && warp == 0))
+          mbar_arrive(bar(ctl->q_full[r]));
       }
       // what this row sees, and what all rows of the row tile see
       const int pos = sp.first + rr / a.group;

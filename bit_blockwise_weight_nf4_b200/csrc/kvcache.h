@@ -1,5 +1,5 @@
 // kvcache.h -- internal interface of the 4-bit key/value cache kernels
-// (kv_cache.cu, attn_decode.cu).  Not part of the public ABI.
+// (kv_cache.cu, attn_decode.cu, attn_prefill.cu).  Not part of the public ABI.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -40,6 +40,9 @@ cudaError_t launch_kv_read(const bnb4_kv_cache& c, const int64_t* slots, int64_t
 
 // Attention over the cache; see bnb_attn_4bit for the arguments.
 size_t attn_workspace_bytes(const bnb4_attn& a);
-cudaError_t launch_attn(const bnb4_attn& a, int num_sms, int* err, cudaStream_t s);
+// wait_limit_ns (0: the usual limit) and withhold != 0 are the failure-detection
+// diagnostic: CTA 0's first wait runs out.
+cudaError_t launch_attn(const bnb4_attn& a, int num_sms, int* err, cudaStream_t s,
+                        uint64_t wait_limit_ns = 0, int withhold = 0);
 
 }  // namespace bnb4

@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define BNB4_ABI_VERSION 5
+#define BNB4_ABI_VERSION 6
 
 /* Every entry point is exported from the shared library (the library is
  * built with hidden visibility by default). */
@@ -528,6 +528,15 @@ BNB4_API int bnb4_device_status(void* stream, int32_t clear);
 BNB4_API int bnb4_debug_gemm_withhold(const void* X, int64_t M, int64_t K,
                                       const bnb4_qstate* W, int64_t N, void* Y,
                                       int32_t wait_limit_us, void* stream);
+
+/*
+ * The same diagnostic for the kernels of bnb_attn_4bit (same arguments and
+ * checks): CTA 0 waits for a copy of cached scales that is never made (few
+ * rows), or for a part of the queries that is never announced (many).  out and
+ * lse receive no defined values.
+ * Errors: as bnb_attn_4bit, INVALID_ARG for the limit.
+ */
+BNB4_API int bnb4_debug_attn_withhold(const bnb4_attn* a, int32_t wait_limit_us, void* stream);
 
 /*
  * Self-check of the quantize kernel's reciprocal (no counterpart on the
