@@ -986,10 +986,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const Prefill
         else
           umma_commit(one, bar(i + 1 < 2 * T ? ctl->o_full[r] : ctl->done[r]));
       }
-      // after a wait that gave up the products in flight still finish before
-      // tensor memory is given back
-      if (lane == 0 && *reinterpret_cast<volatile int*>(&ctl->abort))
-        wait_drain(bar(ctl->done[r]), 0, ctl);
+      // the products in flight finish before tensor memory is given back, also
+      // where the softmax warps gave up waiting for them
+      if (lane == 0) wait_drain(bar(ctl->done[r]), 0, ctl);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
