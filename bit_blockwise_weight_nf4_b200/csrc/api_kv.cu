@@ -40,12 +40,32 @@ int check_strides(int64_t ts, int64_t hs, int64_t per) {
   return ts % per == 0 && hs % per == 0 ? BNB4_OK : BNB4_ERR_ALIGNMENT;
 }
 
+// Whether two of tokens x heads rows of `dim` elements at t * ts + h * hs share an
+// element.
+bool rows_overlap(int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t dim) {
+  if ((tokens > 1 && ts < dim) || (heads > 1 && hs < dim)) return true;
+  if (tokens < 2 || heads < 2) return false;
+  using Wide = __int128;  // a stride may be anything below 2^63
+  // a token's heads end before the next token, or a head's tokens before the next head
+  if (ts >= Wide(hs) * (heads - 1) + dim || hs >= Wide(ts) * (tokens - 1) + dim) return false;
+  // interleaved: rows (t, h + j) and (t + i, h) for the i that bring them nearest
+  const bool by_heads = heads <= tokens;
+  const int64_t n = by_heads ? heads : tokens, m = by_heads ? tokens : heads;
+  const Wide step = by_heads ? hs : ts, other = by_heads ? ts : hs;
+  for (int64_t j = 1; j < n; ++j) {
+    const Wide x = step * j, i = x / other;
+    if ((i >= 1 && i < m && x - i * other < dim) || (i + 1 < m && (i + 1) * other - x < dim))
+      return true;
+  }
+  return false;
+}
+
 // Rows that are written do not lie over one another.
 int check_written(int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t dim,
                   int64_t per) {
   const int rc = check_strides(ts, hs, per);
   if (rc != BNB4_OK) return rc;
-  return (tokens > 1 && ts < dim) || (heads > 1 && hs < dim) ? BNB4_ERR_SHAPE : BNB4_OK;
+  return rows_overlap(ts, hs, tokens, heads, dim) ? BNB4_ERR_SHAPE : BNB4_OK;
 }
 
 int on_device(const void* p) {
@@ -111,6 +131,7 @@ int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, int64_t t
   if (v && (rc = check_written(v_stride_t, v_stride_h, tokens, heads, dim, per)) != BNB4_OK)
     return rc;
   if (!aligned(k, 16) || !aligned(v, 16)) return BNB4_ERR_ALIGNMENT;
+  if (k == v) return BNB4_ERR_SHAPE;  // (both NULL is refused above)
   int sms;
   if ((rc = bnb4::device_sms(&sms)) != BNB4_OK) return rc;
   if (k && (rc = on_device(k)) != BNB4_OK) return rc;

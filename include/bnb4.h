@@ -433,9 +433,10 @@ BNB4_API int bnb_kv_write_4bit(const void* k, int64_t k_stride_t, int64_t k_stri
 /*
  * The cached keys and values of `tokens` slots, dequantized to out_dtype
  * (BNB4_F32, BNB4_BF16 or BNB4_F16): RN_out(RN(t[code] * absmax)).  k or v
- * may be NULL (not read).  Rows of a slot outside the cache are left as they
- * were.  Strides in elements, >= head_dim where there is more than one token
- * or head, multiples of 8 (4 for BNB4_F32).
+ * may be NULL (not wanted).  Rows of a slot outside the cache are left as they
+ * were.  Strides in elements, multiples of 8 (4 for BNB4_F32); rows that share an
+ * element are refused (SHAPE), within k and within v; that k and v lie apart is
+ * the caller's to see to.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, SHAPE, CUDA.
  */
 BNB4_API int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, int64_t tokens,
@@ -469,8 +470,8 @@ BNB4_API int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, 
  *          exp(scale * q . K_j), or NULL.
  *  workspace     bnb4_attn_workspace bytes (0: may be NULL), 16-byte aligned,
  *          any contents; not to be shared by calls that may overlap.
- * All device memory; q and out 16-byte aligned, strides in elements, >= 0
- * (out: >= head_dim where there is more than one row or head), multiples of 8.
+ * All device memory; q and out 16-byte aligned, strides in elements, >= 0,
+ * multiples of 8; rows of out that share an element are refused (SHAPE).
  * Finite scales are taken up to 2^100; a scale that is not finite makes the
  * rows that see its token NaN.  Results repeat bit
  * for bit on a device.  The call reads seq_lens, cu_seqlens_q and block_table

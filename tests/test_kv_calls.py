@@ -1,9 +1,10 @@
 """Calls of the 4-bit key/value cache that are settled on the host, without a
 GPU: what they refuse, and what they answer at once."""
+import numpy as np
 import pytest
 
 import bit_blockwise_weight_nf4_b200 as bnb4
-from test_kv_abi import attn
+from test_kv_abi import A, attn, cache
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -19,3 +20,36 @@ def test_failure_diagnostic_checks_its_limit_and_arguments():
     assert bnb4.bnb4_debug_attn_withhold(attn(out=None), 1000, None) == bnb4.ERR_INVALID_ARG
     assert bnb4.bnb4_debug_attn_withhold(attn(window=-1), 1000, None) == bnb4.ERR_SHAPE
     assert bnb4.bnb4_debug_attn_withhold(attn(batch=0, total_q=0), 1000, None) == bnb4.OK
+
+
+# (tokens, heads, token stride, head stride) in elements, rows of 128: do any two
+# rows share an element?
+OVERLAPS = [(2, 2, 128, 128, True), (2, 2, 256, 128, False), (2, 2, 128, 256, False),
+            (3, 2, 128, 256, True), (3, 2, 128, 384, False), (2, 3, 256, 128, True),
+            (2, 3, 384, 128, False), (2, 2, 384, 256, False), (3, 3, 384, 256, False), (3, 4, 384, 256, True),
+            (3, 2, 384, 512, False), (2, 2, 256, 248, True), (2, 2, 256, 136, True),
+            (1, 8, 0, 128, False), (8, 1, 128, 0, False), (5, 4, 128, 136, True),
+            (4, 5, 136, 128, True), (1000, 2, 128, 128000, False), (1001, 2, 128, 128000, True),
+            (2, 2, 1 << 62, (1 << 62) + 64, True), (2, 3, (1 << 62) + 64, 1 << 61, True),
+            (2, 2, 1 << 62, (1 << 62) + 128, False), (70, 50, 49 * 128, 50 * 128, True),
+            (50, 49, 49 * 128, 50 * 128, False)]
+
+
+@pytest.mark.parametrize("tokens,heads,ts,hs,shared", OVERLAPS)
+def test_rows_that_are_written_do_not_overlap(tokens, heads, ts, hs, shared):
+    rows = np.add.outer(np.arange(tokens, dtype=object) * ts, np.arange(heads, dtype=object) * hs)
+    rows = sorted(rows.ravel())
+    assert shared == any(b - a < 128 for a, b in zip(rows, rows[1:]))
+    c = cache(n_kv_heads=heads)
+    read = lambda *kv: bnb4.bnb_kv_read_4bit(c, A, tokens, *kv, bnb4.BF16, None)
+    fine = (A, heads * 128, 128)
+    got = [read(A, ts, hs, A + (1 << 30), *fine[1:]), read(A + (1 << 30), *fine[1:], A, ts, hs),
+           read(None, 0, 0, A, ts, hs),
+           bnb4.bnb_attn_4bit(attn(cache=c, n_heads=heads, total_q=tokens, batch=tokens,
+                                   out_stride_t=ts, out_stride_h=hs), None)]
+    assert [rc == bnb4.ERR_SHAPE for rc in got] == [shared] * 4, got
+
+
+def test_keys_and_values_are_not_read_into_one_place():
+    got = bnb4.bnb_kv_read_4bit(cache(), A, 2, A, 256, 128, A, 256, 128, bnb4.BF16, None)
+    assert got == bnb4.ERR_SHAPE
