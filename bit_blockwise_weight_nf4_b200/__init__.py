@@ -662,7 +662,7 @@ def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None
         cu = None
     else:
         cu = _index(cu_seqlens_q, cache, i32, (B + 1,), "cu_seqlens_q")
-        if max_q_len is None:
+        if max_q_len is None or T == 0:
             max_q_len = max(1, T)
     lp = None if lse is None else _index(lse, cache, torch.float32, (T, heads), "lse")
     if max_seq_len is None:

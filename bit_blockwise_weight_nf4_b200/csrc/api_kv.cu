@@ -154,7 +154,8 @@ static int check_attn(const bnb4_attn* a) {
     return BNB4_ERR_SHAPE;
   if (a->n_heads < 1 || a->n_heads % a->cache->n_kv_heads != 0) return BNB4_ERR_SHAPE;
   if (static_cast<int64_t>(a->max_q_len) * a->n_heads > INT32_MAX) return BNB4_ERR_SHAPE;
-  if (!a->cu_seqlens_q && static_cast<int64_t>(a->batch) * a->max_q_len != a->total_q)
+  if (!a->cu_seqlens_q && a->total_q != 0 &&
+      static_cast<int64_t>(a->batch) * a->max_q_len != a->total_q)
     return BNB4_ERR_SHAPE;
   if (a->block_table_width < 1 || a->block_table_stride < a->block_table_width ||
       a->block_table_width > (1 << 30) / a->cache->page_size)
@@ -171,7 +172,7 @@ int bnb4_attn_workspace(const bnb4_attn* a, size_t* bytes) {
   if (!bytes) return BNB4_ERR_INVALID_ARG;
   const int rc = check_attn(a);
   if (rc != BNB4_OK) return rc;
-  *bytes = bnb4::attn_workspace_bytes(*a);
+  *bytes = a->batch == 0 || a->total_q == 0 ? 0 : bnb4::attn_workspace_bytes(*a);
   return BNB4_OK;
 }
 

@@ -458,7 +458,7 @@ BNB4_API int bnb_kv_read_4bit(const bnb4_kv_cache* cache, const int64_t* slots, 
  * than its queries) gives zeros and a log-sum-exp of -infinity.
  *  cu_seqlens_q  int32[batch + 1]: sequence b's queries are rows
  *          [cu_seqlens_q[b], cu_seqlens_q[b + 1]) of q and out; or NULL:
- *          max_q_len each (total_q = batch * max_q_len).  Rows of no sequence
+ *          max_q_len each (total_q = batch * max_q_len, or 0: nothing to do).  Rows of no sequence
  *          are left as they were, and so are a sequence's rows behind its
  *          first max_q_len.
  *  seq_lens      int32[batch]; lengths past block_table_width * page_size

@@ -26,7 +26,8 @@ def test_failure_diagnostic_checks_its_limit_and_arguments():
 # rows share an element?
 OVERLAPS = [(2, 2, 128, 128, True), (2, 2, 256, 128, False), (2, 2, 128, 256, False),
             (3, 2, 128, 256, True), (3, 2, 128, 384, False), (2, 3, 256, 128, True),
-            (2, 3, 384, 128, False), (2, 2, 384, 256, False), (3, 3, 384, 256, False), (3, 4, 384, 256, True),
+            (2, 3, 384, 128, False), (2, 2, 384, 256, False), (3, 3, 384, 256, False),
+            (3, 4, 384, 256, True),
             (3, 2, 384, 512, False), (2, 2, 256, 248, True), (2, 2, 256, 136, True),
             (1, 8, 0, 128, False), (8, 1, 128, 0, False), (5, 4, 128, 136, True),
             (4, 5, 136, 128, True), (1000, 2, 128, 128000, False), (1001, 2, 128, 128000, True),
@@ -53,3 +54,12 @@ def test_rows_that_are_written_do_not_overlap(tokens, heads, ts, hs, shared):
 def test_keys_and_values_are_not_read_into_one_place():
     got = bnb4.bnb_kv_read_4bit(cache(), A, 2, A, 256, 128, A, 256, 128, bnb4.BF16, None)
     assert got == bnb4.ERR_SHAPE
+
+
+def test_no_queries_is_an_empty_call():
+    """Sequences without new queries: nothing to do, with and without offsets."""
+    for kw in (dict(), dict(cu_seqlens_q=A)):
+        a = attn(total_q=0, batch=3, q=None, out=None, workspace=None, workspace_bytes=0, **kw)
+        assert bnb4.bnb4_attn_workspace(a) == (bnb4.OK, 0)
+        assert bnb4.bnb_attn_4bit(a, None) == bnb4.OK
+    assert bnb4.bnb_attn_4bit(attn(total_q=0, batch=3, scale=0.0), None) == bnb4.ERR_INVALID_ARG
