@@ -507,6 +507,8 @@ class KVCache4bit:
         dt = BF16 if dtype == torch.bfloat16 else F16 if dtype == torch.float16 else None
         if dt is None:
             raise TypeError("a cache's scales are bfloat16 or float16")
+        if qtype != NF4 and qtype != FP4:
+            raise ValueError("qtype is NF4 or FP4")
         u8 = torch.uint8
         if len(shape) != 4 or blocksize <= 0 or v_codes.shape != shape or \
                 k_codes.dtype != u8 or v_codes.dtype != u8 or v_absmax.dtype != dtype:
@@ -667,6 +669,9 @@ def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None
     lp = None if lse is None else _index(lse, cache, torch.float32, (T, heads), "lse")
     if max_seq_len is None:
         max_seq_len = min(W * cache.page_size, 0x7fffffff)
+    low, high = -0x80000000, 0x7fffffff  # ctypes would cut others to 32 bits
+    if not (low <= max_q_len <= high and low <= max_seq_len <= high and low <= window <= high):
+        raise ValueError("max_q_len, max_seq_len and window are 32-bit integers")
     a = Attn(qp, qt, qh, op, ot, oh, lp, ctypes.pointer(cache.struct), block_table.data_ptr(),
              step[0] if B > 1 else W, lens, cu, None, 0, T, B, heads, max_q_len, max_seq_len, W,
              1 if causal else 0, window, cache.head_dim ** -0.5 if scale is None else scale, 0)

@@ -2,6 +2,7 @@
 GPU: what they refuse, and what they answer at once."""
 import numpy as np
 import pytest
+import torch
 
 import bit_blockwise_weight_nf4_b200 as bnb4
 from test_kv_abi import A, attn, cache
@@ -63,3 +64,29 @@ def test_no_queries_is_an_empty_call():
         assert bnb4.bnb4_attn_workspace(a) == (bnb4.OK, 0)
         assert bnb4.bnb_attn_4bit(a, None) == bnb4.OK
     assert bnb4.bnb_attn_4bit(attn(total_q=0, batch=3, scale=0.0), None) == bnb4.ERR_INVALID_ARG
+
+
+def cpu_call(**kw):
+    """attn_4bit on CPU tensors: a call without a fault fails for the device."""
+    c = bnb4.KVCache4bit.empty(40, 64, 2, 128, torch.bfloat16, 64, bnb4.NF4, device="cpu")
+    q = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
+    bt, sl = torch.zeros(3, 40, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    cu = torch.zeros(4, dtype=torch.int32) if "max_q_len" in kw else None
+    return bnb4.attn_4bit(q, c, bt, sl, cu, **kw)
+
+
+@pytest.mark.parametrize("name", ["window", "max_q_len", "max_seq_len"])
+@pytest.mark.parametrize("value", [(1 << 32) + 5, 1 << 31, -(1 << 32) + 1, 1 << 70])
+def test_numbers_past_32_bits_are_refused(name, value):
+    """They would be cut to their low 32 bits on the way: another window, rows left out."""
+    with pytest.raises(ValueError, match="CUDA device"):
+        cpu_call(**{name: 5})
+    with pytest.raises(ValueError, match=name):
+        cpu_call(**{name: value})
+
+
+def test_code_types_past_32_bits_are_refused():
+    c = bnb4.KVCache4bit.empty(4, 16, 2, 128, torch.bfloat16, 64, bnb4.NF4, device="cpu")
+    for qtype in (1 << 32, (1 << 32) + 1, 2, -1):
+        with pytest.raises(ValueError, match="qtype"):
+            bnb4.KVCache4bit(c.k_codes, c.v_codes, c.k_absmax, c.v_absmax, 64, qtype)
