@@ -682,7 +682,10 @@ def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None
     if need.value:
         if workspace is None:
             workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+        elif not workspace.is_contiguous() or workspace.device != q.device:
+            raise ValueError("workspace is a contiguous tensor on the cache's device")
+        a.workspace = workspace.data_ptr()
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
     rc = _call(lib.bnb_attn_4bit, cache.device_index, ref)
     if rc:
         raise Bnb4Error(rc, "bnb_attn_4bit")

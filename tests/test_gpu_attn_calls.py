@@ -29,3 +29,23 @@ def test_no_queries_is_an_empty_call(ragged, batch):
                                      max_q, 90, 0.1, True, 0, 64, bnb4.NF4)
         assert y.shape == (0, 4, 128)
     torch.cuda.synchronize()
+
+
+def test_workspaces_of_any_element_type():
+    """A workspace's size is its bytes, whatever its elements are."""
+    case = Case([5000, 333], 64, 2, 128, 64, bnb4.NF4, oracle.BF16, seed=51)
+    q, c = case.queries(2, 4).cuda(), case.cache()
+    bt, sl = case.block_table.cuda(), ints(case.kv_lens)
+    want = bnb4.attn_4bit(q, c, bt, sl)
+    a = bnb4.Attn(0, 0, 0, 0, 0, 0, None, bnb4.ctypes.pointer(c.struct), 0, bt.shape[1], 0, None,
+                  None, 0, 2, 2, 4, 1, bt.shape[1] * 64, bt.shape[1], 1, 0, 0.1, 0)
+    rc, need = bnb4.bnb4_attn_workspace(a)
+    assert rc == bnb4.OK and need > 0
+    for dtype in (torch.uint8, torch.float32, torch.int64):
+        ws = torch.empty(-(-need // dtype.itemsize), dtype=dtype, device="cuda")
+        assert torch.equal(bnb4.attn_4bit(q, c, bt, sl, workspace=ws), want)
+    with pytest.raises(bnb4.Bnb4Error):
+        bnb4.attn_4bit(q, c, bt, sl, workspace=torch.empty(need - 1, dtype=torch.uint8,
+                                                           device="cuda"))
+    with pytest.raises(ValueError):
+        bnb4.attn_4bit(q, c, bt, sl, workspace=torch.empty(need, dtype=torch.uint8))

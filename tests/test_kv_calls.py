@@ -90,3 +90,17 @@ def test_code_types_past_32_bits_are_refused():
     for qtype in (1 << 32, (1 << 32) + 1, 2, -1):
         with pytest.raises(ValueError, match="qtype"):
             bnb4.KVCache4bit(c.k_codes, c.v_codes, c.k_absmax, c.v_absmax, 64, qtype)
+
+
+def test_workspaces_are_checked():
+    """A workspace is memory on the cache's device, counted in bytes."""
+    ok = torch.empty(1 << 24, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA device"):
+        cpu_call(workspace=ok)
+    with pytest.raises(ValueError, match="CUDA device"):  # as many bytes in other elements
+        cpu_call(workspace=ok.view(torch.float32))
+    small = torch.empty(16, dtype=torch.uint8)
+    for bad in (small.expand(1 << 20, 16), ok[::2], ok.view(4096, 4096).t(),
+                torch.empty(1 << 24, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            cpu_call(workspace=bad)
