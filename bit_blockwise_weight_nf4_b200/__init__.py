@@ -599,8 +599,9 @@ def kv_write_4bit(k, v, cache, slots):
 def kv_read_4bit(cache, slots, out_dtype=None, out=None):
     """The cached keys and values of ``slots`` (int64 [T]) as two tensors [T,
     kv heads, D] of ``out_dtype`` (fp32, bf16 or fp16; default the cache's
-    dtype), or into ``out`` = (k, v), either of which may be None.  Rows of a
-    slot outside the cache are not written."""
+    dtype), or into ``out`` = (k, v), either of which may be None, with rows
+    that do not overlap.  Rows of a slot outside the cache are not written:
+    they stay as they were in ``out``, and without it hold anything."""
     torch, _, _, lib = _fast()
     T, H, D = slots.shape[0], cache.n_kv_heads, cache.head_dim
     sp = _index(slots, cache, torch.int64, (T,), "slots")
@@ -639,7 +640,11 @@ def attn_4bit(q, cache, block_table, seq_lens, cu_seqlens_q=None, max_q_len=None
     to 1 / sqrt(D); ``window`` > 0 limits how far back a query sees;
     ``lse`` (fp32 [T, heads], contiguous) receives the log-sum-exp.
     ``max_seq_len`` (default: what the block table holds) is the bound by
-    which the work is split."""
+    which the work is split.  Rows of no sequence, and a sequence's rows behind
+    its first ``max_q_len``, are not written: they stay as they were in ``out``,
+    and without it hold anything.  ``workspace`` (contiguous, any element type)
+    is used where the call needs one; calls that may overlap need one each.
+    No gradient is recorded: a cache is not trained."""
     torch, _, _, lib = _fast()
     i32, shape, dtype = torch.int32, q.shape, q.dtype
     T, heads = shape[0], shape[1]

@@ -31,24 +31,34 @@
 //    code; this is ~0.75 and half a load.)
 //  * Precision: q in bf16 is scaled by a power of two per row into fp16
 //    without loss (28 binades below the row's largest stay exact); the table
-//    is multiplied by the constant that brings its fp16 roundings to 6e-5 of
-//    a value's size; weights p a_v are scaled by the running power of two of
+//    is multiplied by the constant that brings NF4's fp16 roundings to 3.6e-5 of
+//    the scale in the mean square, 8.4e-5 at most, up to 3.1e-4 of a value (FP4 is
+//    exact); weights p a_v are scaled by the running power of two of
 //    the block's largest a_v, to at most 2^15, so they stay normal fp16 down
-//    to 2^-29 of it.  For fp16 outputs, whose last place is finer than such a
-//    weight's rounding, the weights are split into two fp16 terms.
+//    to 2^-29 of it.  For fp16 outputs, whose last place is finer than those
+//    roundings, the weights are split into two fp16 terms and the keys' table
+//    entries keep their residue; the values' table stays in one term (a residue
+//    would cost a lookup and a product more each), which leaves 1.1 times the
+//    error of the output's own rounding for NF4.
 //  * Work is split evenly: the tiles of all (sequence, head) pairs form one
 //    line that is cut into equal runs, one per CTA; a run's first and last
 //    pair may be shared with its neighbours, whose partial results (fp32, in
 //    the workspace) a second kernel joins in a fixed order, so results repeat
 //    bit for bit.
 //
-// What bounds it: the instructions around the lookups.  16 sequences of 4096
-// tokens, 32 heads of 128 (bf16, NF4, blocks of 64): 98 us, 2,915 GB/s of cache
-// (44 us at the copy rate); issue slots 55% busy, integer pipe 49%, loads from
-// shared memory 47%, DRAM 37%.  Side by side, 12 warps with tiles of 64 tokens
+// What bounds it: issued instructions.  16 sequences of 4096
+// tokens, 32 heads of 128 (bf16, NF4, blocks of 64): 97 us, 2,940 GB/s of cache
+// (44 us at the copy rate); issue slots 55% busy, integer pipe 50%, loads from
+// shared memory 48%, DRAM 38%.  A warp issues 1,584 instructions per tile of 64
+// tokens, of which the lookups (256 permutes, 256 loads) and the products (64)
+// are 576; most of the others are scores, exponentials, weights and transposes,
+// where with one row per head 7 of 8 columns are padding.  At 168 registers a
+// thread the instantiations with heads of 128 spill: 8 to 180 bytes up to 8 rows,
+// 92 to 692 (fp16, NF4, blocks of 32) for 9 to 16.
+// Side by side, 12 warps with tiles of 64 tokens
 // took 93 us when 16 warps took 99 and 8 warps with tiles of 128 tokens 95.
-// 24 ragged sequences with 4 rows per head 64 us, 2 x 131072 tokens 92 us, 12
-// sequences with 16 rows (fp16, blocks of 32; weights in two terms) 75 us,
+// 24 ragged sequences with 4 rows per head 64 us, 2 x 131072 tokens 90 us, 12
+// sequences with 16 rows (fp16, blocks of 32; weights in two terms) 78 us,
 // one sequence of 257 tokens 9.7 us, most of it the launch and three loads in
 // a row (lengths, page table, cache).
 #include "attn.cuh"
@@ -1110,8 +1120,9 @@ cudaError_t launch_f(AttnArgs& a, int rows, int64_t span, int num_sms, cudaStrea
 
 }  // namespace
 
-// At most this many rows per (sequence, key/value head) run here; more go to
-// the tensor-core kernel, whose tiles have 256 rows.  At 16 rows and 12 sequences
+// At most this many rows per (sequence, key/value head) run here, as many as the
+// registers hold sums for; more go to the tensor-core kernel, whose tiles have
+// 256 rows, padded or not.  At 16 rows and 12 sequences
 // of about 3000 tokens this kernel takes 56 us, that one 73 (bf16) to 121 (fp16);
 // with little cache to read the two are alike.
 constexpr int64_t kMaxRows = 16;

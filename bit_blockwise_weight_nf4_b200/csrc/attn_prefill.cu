@@ -59,11 +59,15 @@
 // scaling by the power of two of their tile's largest scale, values by a running
 // one, both to at most 2^16, and weights by 2^7 (so at most 2^15): keys and values
 // stay normal 24 binades below the largest, whether a row sees that one or not,
-// weights 21.  For fp16 caches, whose outputs' last place is finer than those
+// weights 21.  Of bf16 caches an NF4 key is off by the table's rounding and the
+// product's, 2.3e-4 of itself in the mean square, which the scores carry into the
+// exponent: next to the error of fp32 weights 1.03 times it at scores of a
+// standard deviation of 1, 1.14 at 10, 1.41 at 30 (FP4's products are exact:
+// 1.01).  For fp16 caches, whose outputs' last place is finer than those
 // roundings, keys, values and weights are kept in two fp16 terms (twice the
 // products for the scores, three times for the sums; in one term the weights'
 // rounding made up to 1.56 times the error of exact fp32 weights).  The prompts
-// above take 217 us in fp16.
+// above take 222 us in fp16.
 // Every mbarrier wait is bounded; no TMA load is used.
 #include "attn.cuh"
 #include "common.cuh"

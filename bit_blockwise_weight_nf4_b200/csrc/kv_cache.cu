@@ -20,7 +20,8 @@
 // slot is looked up once.  Reading, the next unit's rows are loaded before this
 // one's are decoded (its slot a unit earlier still): the latency of two loads
 // in a row was most of the time (65536 tokens of 32 heads of 128, bf16: 390 us
-// without, 264 us with, 5,140 GB/s).  Writing, whose work per value is longer,
+// without, 264 us with, 5,140 GB/s, replayed in a graph; 280 to 290 us, 4,700 to
+// 4,850 GB/s, on inputs that are new each time).  Writing, whose work per value is longer,
 // that gained nothing.  Table lookups are warp shuffles (the table is one entry
 // per lane: no shared memory to fill, which a 16-token call would wait for):
 // two per value to quantize, one to decode.  Writing 2048 tokens of 32 heads of

@@ -25,9 +25,9 @@ from typing import Optional, Tuple
 import torch
 
 from . import (BF16, F16, KVCache4bit, NF4, QState, _check, attn_4bit as _attn_4bit,
-               kv_read_4bit as _kv_read_4bit, kv_write_4bit as _kv_write_4bit, _stream, bnb_dequantize_4bit, bnb_gemm_4bit,
-               bnb_gemv_4bit, bnb_linear_4bit, bnb_quantize_4bit, bnb_quantize_4bit_2d,
-               workspace_for, QuantState)
+               kv_read_4bit as _kv_read_4bit, kv_write_4bit as _kv_write_4bit, _stream,
+               bnb_dequantize_4bit, bnb_gemm_4bit, bnb_gemv_4bit, bnb_linear_4bit,
+               bnb_quantize_4bit, bnb_quantize_4bit_2d, workspace_for, QuantState)
 
 Tensor = torch.Tensor
 _DTYPES = {torch.float32: 0, torch.bfloat16: BF16, torch.float16: F16}
